@@ -492,6 +492,157 @@ int pkv_append_and_decode_fp8(const void* k_new, const void* v_new, int32_t src_
                               float k_scale, float v_scale, int32_t partition_tokens,
                               void* workspace, size_t workspace_bytes, float* out, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Rotary positions.                                                        */
+/*                                                                          */
+/* Channel pair i (0 <= i < rot_dim / 2) of every head of a token at         */
+/* position p is turned by angle = p * inv_freq[i]:                          */
+/*     y_a = x_a c - x_b s,  y_b = x_a s + x_b c,                            */
+/*     c = factor cos(angle),  s = factor sin(angle).                        */
+/* interleaved = 0: (a, b) = (i, i + rot_dim / 2); 1: (2i, 2i + 1).  Channels */
+/* from rot_dim on pass through unchanged.  Angles are formed in 64 bits, the */
+/* rest in 32, each output rounded once.                                     */
+/* ------------------------------------------------------------------------ */
+
+enum pkv_rope_scaling_kind {
+  PKV_ROPE_PLAIN = 0,  /* f_i = base^(-2i / rot_dim) */
+  PKV_ROPE_LINEAR = 1, /* f_i / scale */
+  PKV_ROPE_BASE = 2,   /* base * scale^(rot_dim / (rot_dim - 2)) in place of base */
+  PKV_ROPE_BANDS = 3,  /* by turns r_i = original_positions f_i / 2 pi: f_i / scale up to `slow` turns, f_i from
+                          `fast` on, between them a blend linear in r_i */
+  PKV_ROPE_YARN = 4    /* the blend linear in i, between the pairs that make `fast` turns (rounded down) and `slow`
+                          turns (rounded up) over the original positions; factor = 0.1 ln(scale) + 1 */
+};
+
+typedef struct pkv_rope_scaling {
+  int32_t kind;               /* enum pkv_rope_scaling_kind */
+  int32_t original_positions; /* BANDS, YARN: positions before scaling, > 0 */
+  double scale;               /* >= 1 (all kinds but PLAIN) */
+  double slow, fast;          /* BANDS, YARN: 0 < slow < fast */
+} pkv_rope_scaling_t;
+
+/* Frequencies for the calls below: inv_freq (host, double[rot_dim / 2]) and
+ * the factor, from `base` (> 1) and a scaling for long contexts (NULL:
+ * PLAIN).  Host only.  Errors: INVALID_ARG, UNSUPPORTED (kind). */
+int pkv_rope_frequencies(int32_t rot_dim, double base, const pkv_rope_scaling_t* scaling, double* inv_freq,
+                         float* factor);
+
+/* Rotates x into out: dtype[n_tokens][num_heads][head_dim], tokens x_stride
+ * and out_stride elements apart (at least num_heads * head_dim, a multiple of
+ * 16 bytes; heads and channels packed).  positions: int32[n_tokens] on the
+ * device, any value; inv_freq: double[rot_dim / 2] on the device.
+ * transpose = 1 applies the transposed map (s negated): the gradient of x
+ * from that of out.  out may be x (with the same stride), but must not
+ * overlap it otherwise.  dtype F32, BF16 or F16; head_dim a multiple of 8, at
+ * most 512; rot_dim even, 2 .. head_dim. */
+int pkv_rope(const void* x, int64_t x_stride, const int32_t* positions, const double* inv_freq, int32_t n_tokens,
+             int32_t num_heads, int32_t head_dim, int32_t rot_dim, int32_t interleaved, float factor,
+             int32_t transpose, int32_t dtype, void* out, int64_t out_stride, void* stream);
+
+/* pkv_kv_append with the rotation on the way: q rotated into q_out
+ * (dtype[n_tokens][num_q_heads][head_dim], packed), K rotated and V as it is
+ * into slot slot_mapping[i] of the pools, in one launch.  q, k, v:
+ * dtype[n_tokens][heads][head_dim] with token strides as for pkv_rope, so that
+ * the three may be views of one projection's output.  Slots as for
+ * pkv_kv_append (slot < 0: q is rotated, nothing is written to the pools).
+ * num_q_heads = 0 leaves q and q_out out.  head_dim 64 or 128, block_size 8,
+ * 16 or 32.  q_out must not overlap q. */
+int pkv_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const int32_t* positions, const double* inv_freq, const int32_t* slot_mapping,
+                    int32_t n_tokens, void* q_out, void* k_pool, void* v_pool, int32_t num_blocks,
+                    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t rot_dim,
+                    int32_t interleaved, float factor, int32_t dtype, void* stream);
+
+/* The same into e4m3 pools: the rotated K and V in fp32 times 1 / scale,
+ * rounded once to codes as by pkv_kv_append_fp8; q_out is float16 whatever
+ * src_dtype, as pkv_paged_attention_decode_fp8 takes it. */
+int pkv_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, int32_t src_dtype, const int32_t* positions, const double* inv_freq,
+                        const int32_t* slot_mapping, int32_t n_tokens, void* q_out, void* k_pool, void* v_pool,
+                        int32_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t block_size, int32_t rot_dim, int32_t interleaved, float factor, float k_scale,
+                        float v_scale, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Block-sparse decode: attention over the blocks that a cheap score selects */
+/* for each query.  dtype is that of the K/V pools and of the bounds; with   */
+/* PKV_FP8_E4M3 (head_dim 128) q is float16.                                 */
+/* ------------------------------------------------------------------------ */
+
+/* Bounds of the keys of each block: bounds[block][kv head][0][d] is the
+ * smallest and [1][d] the largest value of channel d over the block's tokens
+ * (dtype[num_blocks][num_kv_heads][2][head_dim], 16-byte aligned; e4m3: codes).
+ * Rewritten are the bounds of every block that holds one of the last
+ * new_tokens[b] tokens of sequence b (int32[num_seqs] on the device, at most
+ * max_new_tokens each; NULL: one token each, a decode step, none for an empty
+ * sequence), over all of the block's tokens below seq_lens[b]; no others.
+ * Call it after the append.  NaN keys give NaN bounds.  A sequence whose
+ * length is outside its table or whose new_tokens is negative, above
+ * max_new_tokens or above its length is skipped and recorded as
+ * PKV_ERR_INVALID_ARG, a block id outside the pool as PKV_ERR_BAD_BLOCK (that
+ * block is skipped). */
+int pkv_block_bounds(const void* k_pool, const int32_t* block_tables, const int32_t* seq_lens,
+                     const int32_t* new_tokens, int32_t max_new_tokens, int32_t num_seqs, int32_t num_blocks,
+                     int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size,
+                     int32_t dtype, void* bounds, void* stream);
+
+/* Bytes of device workspace pkv_block_select needs.  Host only. */
+int pkv_select_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq, size_t* bytes);
+
+/* For each sequence b and KV head g the blocks to attend over:
+ * selected[b][g][0 .. max_selected) = logical block indices (positions in
+ * the sequence's table), ascending, -1 behind the last.  A sequence of at
+ * most max_selected blocks gets all of them.  Otherwise: its first n_first
+ * and last n_last blocks, and of the others those with the highest
+ *     score[j] = max over the group's heads h of
+ *                sum_d min(q_hd, 0) lo_jd + max(q_hd, 0) hi_jd,
+ * an upper bound of q.k over the block's keys; max_selected in all.  The
+ * ranking is that of 64-bit sums; equal scores go to the lower index, NaN
+ * ranks above every number.  q: dtype[num_seqs][num_q_heads][head_dim];
+ * bounds from pkv_block_bounds; n_first + n_last <= max_selected;
+ * num_q_heads / num_kv_heads in {1, 2, 4, 8}; max_blocks_per_seq at most 2^20.
+ * workspace: at least pkv_select_workspace_size() bytes, 256-byte aligned,
+ * scratch for the duration of the call.  A length outside the table is
+ * recorded as PKV_ERR_INVALID_ARG and selects nothing; block ids outside the
+ * pool are recorded as PKV_ERR_BAD_BLOCK and block 0 is read instead. */
+int pkv_block_select(const void* q, const void* bounds, const int32_t* block_tables, const int32_t* seq_lens,
+                     int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                     int32_t num_blocks, int32_t max_blocks_per_seq, int32_t block_size, int32_t max_selected,
+                     int32_t n_first, int32_t n_last, int32_t dtype, void* workspace, size_t workspace_bytes,
+                     int32_t* selected, void* stream);
+
+/* Bytes of device workspace the block-sparse decode needs.  Host only. */
+int pkv_sparse_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t max_selected, int32_t block_size, int32_t dtype, size_t* bytes);
+
+/* pkv_paged_attention_decode over the tokens of the selected blocks only:
+ * the softmax of sequence b and KV head g runs over the tokens below
+ * seq_lens[b] of the blocks selected[b][g][...] (int32[num_seqs][num_kv_heads]
+ * [max_selected], logical indices, strictly ascending, -1 behind the last).
+ * A list ends at its first negative entry, and at one that is not above its
+ * predecessor or lies beyond the sequence, which is recorded as
+ * PKV_ERR_INVALID_ARG.  An empty list gives zeros.  A length outside the
+ * table is recorded as PKV_ERR_INVALID_ARG and gives zeros, a block id outside
+ * the pool as PKV_ERR_BAD_BLOCK (block 0 is read instead).  fp32 pools: up to
+ * 4 query heads per KV head.  workspace: at least
+ * pkv_sparse_workspace_size() bytes, 256-byte aligned, scratch for the
+ * duration of the call. */
+int pkv_paged_attention_decode_sparse(const void* q, const void* k_pool, const void* v_pool,
+                                      const int32_t* block_tables, const int32_t* seq_lens, const int32_t* selected,
+                                      int32_t max_selected, int32_t num_seqs, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                      int32_t max_blocks_per_seq, int32_t block_size, float scale, int32_t dtype,
+                                      void* workspace, size_t workspace_bytes, float* out, void* stream);
+
+/* The same over e4m3 pools (q float16, head_dim 128). */
+int pkv_paged_attention_decode_sparse_fp8(const void* q, const void* k_pool, const void* v_pool,
+                                          const int32_t* block_tables, const int32_t* seq_lens,
+                                          const int32_t* selected, int32_t max_selected, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t num_blocks, int32_t max_blocks_per_seq, int32_t block_size,
+                                          float scale, float k_scale, float v_scale, void* workspace,
+                                          size_t workspace_bytes, float* out, void* stream);
+
 /* Synchronise `stream`, then read the device status word of the current
  * device into *status: PKV_OK, or the first PKV_ERR_BAD_BLOCK /
  * PKV_ERR_DEVICE_TIMEOUT a kernel recorded since the last clear.  clear != 0

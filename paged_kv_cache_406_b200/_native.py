@@ -44,6 +44,12 @@ class pkv_pool_t(ctypes.Structure):
                 ("max_blocks_per_seq", ctypes.c_int32), ("num_seqs", ctypes.c_int32)]
 
 
+class pkv_rope_scaling_t(ctypes.Structure):
+    """A scaling of rotary frequencies for long contexts (pkv_rope_frequencies)."""
+    _fields_ = [("kind", ctypes.c_int32), ("original_positions", ctypes.c_int32), ("scale", ctypes.c_double),
+                ("slow", ctypes.c_double), ("fast", ctypes.c_double)]
+
+
 _ppool = ctypes.POINTER(pkv_pool_t)
 
 SIGNATURES = {
@@ -87,6 +93,22 @@ SIGNATURES = {
                                                    _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp, _vp]),
     "pkv_prefill_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
     "pkv_decode_pools_workspace_size": (ctypes.c_int, [_ppool, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
+    "pkv_rope_frequencies": (ctypes.c_int, [_i32, ctypes.c_double, ctypes.POINTER(pkv_rope_scaling_t),
+                                            ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_f32)]),
+    "pkv_rope": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _vp, _i64, _vp]),
+    "pkv_rope_append": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32,
+                                       _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp]),
+    "pkv_rope_append_fp8": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
+                                           _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _f32, _vp]),
+    "pkv_block_bounds": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "pkv_select_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, ctypes.POINTER(_sz)]),
+    "pkv_block_select": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                        _i32, _vp, _sz, _vp, _vp]),
+    "pkv_sparse_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
+    "pkv_paged_attention_decode_sparse": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                                         _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp, _vp]),
+    "pkv_paged_attention_decode_sparse_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                                             _i32, _i32, _i32, _f32, _f32, _f32, _vp, _sz, _vp, _vp]),
     "pkv_append_and_decode_pools": (ctypes.c_int, [_ppool, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _i32,
                                                    _i32, _vp, _sz, _vp, _vp]),
 }

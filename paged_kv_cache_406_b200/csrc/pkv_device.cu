@@ -14,11 +14,14 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "append.cuh"
+#include "block_select.cuh"
 #include "decode.cuh"
 #include "decode_mma.cuh"
 #include "decode_tc8.cuh"
 #include "device_common.cuh"
 #include "prefill.cuh"
+#include "rope.cuh"
+#include "sparse_decode.cuh"
 #include "pkv_internal.h"
 
 // ===========================================================================
@@ -1408,3 +1411,9 @@ extern "C" int pkv_decode_step_host(pkv_alloc_t* a, const int64_t* seq_ids, int3
   }
   return pkv::ok();
 }
+
+// ===========================================================================
+// Rotary positions, block bounds and selection, block-sparse decode
+// ===========================================================================
+#include "rope_api.cuh"
+#include "sparse_api.cuh"

@@ -1,0 +1,311 @@
+"""Tensor-level binding of the rotary and block-sparse entry points.
+
+As in ``binding.py`` every function has the name of the C entry point it
+calls, checks its tensors and forwards pointers, sizes and the stream that is
+current on the tensors' device; the tensors of a call lie on one device, which
+need not be the current one.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _native as N
+from ._native import check, lib
+from .binding import _DTYPES, _dtype_code
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
+
+
+def _issue(fn, dev: int, *args) -> None:
+    """One library call on ``dev`` and the stream current there."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc:
+        check(rc)
+
+
+def _on(t: torch.Tensor, name: str, dev: Optional[int] = None, dtype=None, packed: bool = True) -> int:
+    """Checks a tensor; returns its device's index."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if packed and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    d = t.get_device()
+    if dev is not None and d != dev:
+        raise ValueError(f"{name} is on device {d}, the other tensors are on device {dev}")
+    return d
+
+
+def _rows(t: torch.Tensor, name: str, dev: Optional[int], dtype=None):
+    """Checks ``[n_tokens, heads, head_dim]`` with packed heads; returns its
+    sizes and the token stride."""
+    _on(t, name, dev, dtype, packed=False)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
+    n, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        raise ValueError(f"the heads and channels of {name} must be packed (only the token stride is free)")
+    return n, heads, d, s0 if n > 1 else heads * d
+
+
+def _positions(positions: torch.Tensor, inv_freq: torch.Tensor, n: int, dev: int) -> int:
+    _on(positions, "positions", dev, torch.int32)
+    _on(inv_freq, "inv_freq", dev, torch.float64)
+    if positions.numel() != n:
+        raise ValueError("positions must hold one position per token")
+    return 2 * inv_freq.numel()
+
+
+def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor, dev: int):
+    _on(k_pool, "k_pool", dev)
+    _on(v_pool, "v_pool", dev, k_pool.dtype)
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must both be [num_blocks, num_kv_heads, block_size, head_dim]")
+    return k_pool.shape
+
+
+def pkv_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", scale: float = 1.0,
+                         original_positions: int = 0, slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """``(inv_freq, factor)``: float64 frequencies ``[rot_dim / 2]`` on
+    ``device`` and the factor of sines and cosines.  ``scaling`` for contexts
+    longer than ``original_positions``: "plain", "linear", "base", "bands" or
+    "yarn" (the formulas are beside the C declaration)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+    out = (ctypes.c_double * max(1, rot_dim // 2))()
+    factor = ctypes.c_float(0)
+    sc = N.pkv_rope_scaling_t(_SCALINGS[scaling], int(original_positions), float(scale), float(slow), float(fast))
+    check(lib().pkv_rope_frequencies(rot_dim, float(base), ctypes.byref(sc), out, ctypes.byref(factor)))
+    return torch.tensor(list(out), dtype=torch.float64, device=device), factor.value
+
+
+def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
+             factor: float = 1.0, transpose: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotates the first ``2 * len(inv_freq)`` channels of every head of ``x``
+    ``[n_tokens, heads, head_dim]`` (float32, bfloat16 or float16; any token
+    stride) by ``positions * inv_freq``; returns ``out`` (``x`` itself for in
+    place).  ``transpose`` applies the transposed map, which takes the
+    gradient of the result to that of ``x``."""
+    n, heads, d, stride = _rows(x, "x", None)
+    dev = x.get_device()
+    rot = _positions(positions, inv_freq, n, dev)
+    if x.dtype not in _DTYPES or x.dtype in _E4M3:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    if out is None:
+        out = torch.empty((n, heads, d), dtype=x.dtype, device=x.device)
+        ostride = heads * d
+    else:
+        on, oheads, od, ostride = _rows(out, "out", dev, x.dtype)
+        if (on, oheads, od) != (n, heads, d):
+            raise ValueError("out has the wrong shape")
+    _issue(lib().pkv_rope, dev, x.data_ptr(), stride, positions.data_ptr(), inv_freq.data_ptr(), n, heads, d, rot,
+           int(interleaved), float(factor), int(transpose), _DTYPES[x.dtype], out.data_ptr(), ostride)
+    return out
+
+
+def _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, q_dtype):
+    n, hkv, d, ks = _rows(k, "k", None)
+    dev = k.get_device()
+    n2, hkv2, d2, vs = _rows(v, "v", dev, k.dtype)
+    nq, hq, dq, qs = _rows(q, "q", dev, k.dtype)
+    nb, ph, bs, pd = _pools(k_pool, v_pool, dev)
+    if (n2, hkv2, d2) != (n, hkv, d) or (nq, dq) != (n, d) or (ph, pd) != (hkv, d):
+        raise ValueError(f"q, k, v must be [n_tokens, heads, {pd}] with {ph} heads in k and v")
+    rot = _positions(positions, inv_freq, n, dev)
+    _on(slot_mapping, "slot_mapping", dev, torch.int32)
+    if slot_mapping.numel() != n:
+        raise ValueError("slot_mapping must hold one slot per new token")
+    if k.dtype not in _DTYPES or k.dtype in _E4M3:
+        raise TypeError(f"q, k, v must be float32, bfloat16 or float16, got {k.dtype}")
+    if q_out is None:
+        q_out = torch.empty((n, hq, d), dtype=q_dtype, device=k.device)
+    else:
+        _on(q_out, "q_out", dev, q_dtype)
+        if tuple(q_out.shape) != (n, hq, d):
+            raise ValueError("q_out has the wrong shape")
+        if n and q_out.data_ptr() == q.data_ptr():
+            raise ValueError("q_out must not be q")
+    return dev, rot, (qs, ks, vs), (nb, hq, hkv, d, bs), q_out
+
+
+def pkv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                    inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                    interleaved: bool = False, factor: float = 1.0,
+                    q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """:func:`pkv_kv_append` with the rotation of :func:`pkv_rope` on the way:
+    K rotated and V as it is into their slots (``slot < 0`` = padding), q
+    rotated into ``q_out``, which is returned.  q, k, v ``[n_tokens, heads,
+    head_dim]`` may be views of one projection's output."""
+    if k_pool.dtype != k.dtype:
+        raise TypeError(f"k is {k.dtype}, the pools are {k_pool.dtype}")
+    dev, rot, (qs, ks, vs), (nb, hq, hkv, d, bs), q_out = _append_args(
+        q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, k.dtype)
+    _issue(lib().pkv_rope_append, dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+           inv_freq.data_ptr(), slot_mapping.data_ptr(), k.shape[0], q_out.data_ptr(), k_pool.data_ptr(),
+           v_pool.data_ptr(), nb, hq, hkv, d, bs, rot, int(interleaved), float(factor), _DTYPES[k.dtype])
+    return q_out
+
+
+def pkv_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                        inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_pool: torch.Tensor,
+                        v_pool: torch.Tensor, k_scale: float, v_scale: float, interleaved: bool = False,
+                        factor: float = 1.0, q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """:func:`pkv_rope_append` into e4m3 pools (x / scale rounded once to its
+    code); the returned q is float16."""
+    if k_pool.dtype not in _E4M3:
+        raise TypeError(f"the pools must hold e4m3 codes, got {k_pool.dtype}")
+    dev, rot, (qs, ks, vs), (nb, hq, hkv, d, bs), q_out = _append_args(
+        q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, torch.float16)
+    _issue(lib().pkv_rope_append_fp8, dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[k.dtype],
+           positions.data_ptr(), inv_freq.data_ptr(), slot_mapping.data_ptr(), k.shape[0], q_out.data_ptr(),
+           k_pool.data_ptr(), v_pool.data_ptr(), nb, hq, hkv, d, bs, rot, int(interleaved), float(factor),
+           float(k_scale), float(v_scale))
+    return q_out
+
+
+def _batch(block_tables: torch.Tensor, seq_lens: torch.Tensor, dev: int):
+    _on(block_tables, "block_tables", dev, torch.int32)
+    _on(seq_lens, "seq_lens", dev, torch.int32)
+    b = seq_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and seq_lens [num_seqs]")
+    return b, block_tables.shape[1]
+
+
+def pkv_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, bounds: torch.Tensor,
+                     new_tokens: Optional[torch.Tensor] = None, max_new_tokens: int = 1) -> torch.Tensor:
+    """Rewrites, in ``bounds`` ``[num_blocks, num_kv_heads, 2, head_dim]`` (the
+    pool's dtype), the smallest and largest key of every block that holds one
+    of the last ``new_tokens`` tokens of a sequence (int32 ``[num_seqs]``;
+    None: one each); returns ``bounds``."""
+    dev = _on(k_pool, "k_pool")
+    if k_pool.dim() != 4:
+        raise ValueError("k_pool must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    nb, hkv, bs, d = k_pool.shape
+    _on(bounds, "bounds", dev, k_pool.dtype)
+    if tuple(bounds.shape) != (nb, hkv, 2, d):
+        raise ValueError(f"bounds must be [{nb}, {hkv}, 2, {d}]")
+    b, maxb = _batch(block_tables, seq_lens, dev)
+    if new_tokens is not None:
+        _on(new_tokens, "new_tokens", dev, torch.int32)
+        if new_tokens.numel() != b:
+            raise ValueError("new_tokens must be [num_seqs]")
+    _issue(lib().pkv_block_bounds, dev, k_pool.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+           None if new_tokens is None else new_tokens.data_ptr(), int(max_new_tokens), b, nb, hkv, d, maxb, bs,
+           _dtype_code(k_pool), bounds.data_ptr())
+    return bounds
+
+
+def pkv_select_workspace_size(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int) -> int:
+    """Workspace bytes of :func:`pkv_block_select`."""
+    out = ctypes.c_size_t(0)
+    check(lib().pkv_select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq, ctypes.byref(out)))
+    return out.value
+
+
+def pkv_block_select(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     max_selected: int, block_size: int, n_first: int = 1, n_last: int = 2,
+                     selected: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The blocks each (sequence, KV head) attends over: ``selected`` int32
+    ``[num_seqs, num_kv_heads, max_selected]``, ascending logical block
+    indices, -1 behind the last - the first ``n_first`` and last ``n_last``
+    blocks and the best-scored of the others (see the C declaration)."""
+    dev = _on(bounds, "bounds")
+    if bounds.dim() != 4 or bounds.shape[2] != 2:
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    nb, hkv, _, d = bounds.shape
+    b, maxb = _batch(block_tables, seq_lens, dev)
+    _on(q, "q", dev, torch.float16 if bounds.dtype in _E4M3 else bounds.dtype)
+    if q.dim() != 3 or q.shape[0] != b or q.shape[2] != d:
+        raise ValueError(f"q must be [{b}, num_q_heads, {d}]")
+    if selected is None:
+        selected = torch.empty((b, hkv, max_selected), dtype=torch.int32, device=q.device)
+    else:
+        _on(selected, "selected", dev, torch.int32)
+        if tuple(selected.shape) != (b, hkv, max_selected):
+            raise ValueError("selected has the wrong shape")
+    if workspace is None:
+        workspace = torch.empty(pkv_select_workspace_size(b, hkv, maxb), dtype=torch.uint8, device=q.device)
+    else:
+        _on(workspace, "workspace", dev, torch.uint8)
+    _issue(lib().pkv_block_select, dev, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), b,
+           q.shape[1], hkv, d, nb, maxb, int(block_size), int(max_selected), int(n_first), int(n_last),
+           _dtype_code(bounds), workspace.data_ptr(), workspace.numel(), selected.data_ptr())
+    return selected
+
+
+def pkv_sparse_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_selected: int,
+                              block_size: int, dtype: torch.dtype) -> int:
+    """Workspace bytes of the block-sparse decode over pools of ``dtype``."""
+    out = ctypes.c_size_t(0)
+    check(lib().pkv_sparse_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_selected, block_size,
+                                          _DTYPES[dtype], ctypes.byref(out)))
+    return out.value
+
+
+def _sparse(fn, q, k_pool, v_pool, block_tables, seq_lens, selected, tail, q_dtype, out, workspace):
+    dev = _on(k_pool, "k_pool")
+    nb, hkv, bs, d = _pools(k_pool, v_pool, dev)
+    b, maxb = _batch(block_tables, seq_lens, dev)
+    _on(q, "q", dev, q_dtype)
+    if q.dim() != 3 or q.shape[0] != b or q.shape[2] != d:
+        raise ValueError(f"q must be [{b}, num_q_heads, {d}]")
+    _on(selected, "selected", dev, torch.int32)
+    if selected.dim() != 3 or selected.shape[:2] != (b, hkv):
+        raise ValueError(f"selected must be [{b}, {hkv}, max_selected]")
+    hq, k = q.shape[1], selected.shape[2]
+    if out is None:
+        out = torch.empty((b, hq, d), dtype=torch.float32, device=q.device)
+    else:
+        _on(out, "out", dev, torch.float32)
+        if tuple(out.shape) != (b, hq, d):
+            raise ValueError("out has the wrong shape")
+    if workspace is None:
+        workspace = torch.empty(pkv_sparse_workspace_size(b, hq, hkv, d, k, bs, k_pool.dtype), dtype=torch.uint8,
+                                device=q.device)
+    else:
+        _on(workspace, "workspace", dev, torch.uint8)
+    _issue(fn, dev, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+           selected.data_ptr(), k, b, hq, hkv, d, nb, maxb, bs, *tail, workspace.data_ptr(), workspace.numel(),
+           out.data_ptr())
+    return out
+
+
+def pkv_paged_attention_decode_sparse(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                                      block_tables: torch.Tensor, seq_lens: torch.Tensor, selected: torch.Tensor,
+                                      scale: float, out: Optional[torch.Tensor] = None,
+                                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """:func:`pkv_paged_attention_decode` over the tokens of the selected
+    blocks only (``selected`` as :func:`pkv_block_select` returns it); float32
+    ``[num_seqs, num_q_heads, head_dim]``, zeros for an empty selection."""
+    return _sparse(lib().pkv_paged_attention_decode_sparse, q, k_pool, v_pool, block_tables, seq_lens, selected,
+                   (float(scale), _dtype_code(k_pool)), k_pool.dtype, out, workspace)
+
+
+def pkv_paged_attention_decode_sparse_fp8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                                          block_tables: torch.Tensor, seq_lens: torch.Tensor, selected: torch.Tensor,
+                                          scale: float, k_scale: float, v_scale: float,
+                                          out: Optional[torch.Tensor] = None,
+                                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The same over e4m3 pools (q float16)."""
+    if k_pool.dtype not in _E4M3:
+        raise TypeError(f"the pools must hold e4m3 codes, got {k_pool.dtype}")
+    return _sparse(lib().pkv_paged_attention_decode_sparse_fp8, q, k_pool, v_pool, block_tables, seq_lens, selected,
+                   (float(scale), float(k_scale), float(v_scale)), torch.float16, out, workspace)
+
+
+__all__ = ["pkv_rope_frequencies", "pkv_rope", "pkv_rope_append", "pkv_rope_append_fp8", "pkv_block_bounds",
+           "pkv_select_workspace_size", "pkv_block_select", "pkv_sparse_workspace_size",
+           "pkv_paged_attention_decode_sparse", "pkv_paged_attention_decode_sparse_fp8"]
