@@ -8,9 +8,9 @@
 // over the block's keys k and the heads h of the group:
 //     score = max_h sum_d ( min(q_hd, 0) lo_jd + max(q_hd, 0) hi_jd ).
 // The first n_first and last n_last blocks and the best of the others are
-// selected; the ranking is that of exact arithmetic (ties to the lower index):
-// score_kernel computes 32-bit scores with a bound of their error, and
-// select_kernel scores the blocks near the border again in 64 bits.
+// selected; the ranking is that of 64-bit sums (ties to the lower index):
+// select_kernel computes 32-bit scores with a bound of their error and scores
+// the blocks near the border again in 64 bits.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -197,24 +197,45 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// scores in 32 bits
+// selection: a cluster of CTAs per (sequence, KV head)
+//
+// Bytes bound the scoring: 2 D elements per block and KV head, read once for
+// the G heads of the group.  The CTAs of a cluster take equal slices of the
+// row's blocks, 16 blocks a warp at a time, and write 32-bit scores to the
+// workspace; rank 0 then selects (the others leave), so that the selection
+// of one row runs under the scoring of others and needs no launch of its own.
 // ---------------------------------------------------------------------------
+struct SelectStats {  // of one CTA's scores
+  uint32_t min_key, max_key;  // candidates' keys
+  float big;                  // largest |bound|
+  float pad;
+};
+
 struct SelectArgs {
   const void* q;       // dtype[num_seqs][num_q_heads][D]; f16 for e4m3 bounds
   const void* bounds;
   const int32_t* block_tables;
   const int32_t* seq_lens;
-  float* scores;       // [num_seqs * num_kv_heads][width]
-  float* chunk_max;    // [num_seqs * num_kv_heads][chunks]: largest |bound| of a chunk
-  double* fine;        // [num_seqs * num_kv_heads][width]: 64-bit scores, where there are too many for shared memory
+  float* scores;       // [num_seqs * num_kv_heads][max_blocks]
+  SelectStats* stats;  // [num_seqs * num_kv_heads][kSelectCluster]
+  uint64_t* fine;      // [num_seqs * num_kv_heads][max_blocks]: 64-bit keys, where there are too many for shared memory
   int32_t* selected;   // [num_seqs][num_kv_heads][max_selected]
   int32_t num_seqs, num_q_heads, num_kv_heads, num_blocks, max_blocks, block_size;
   int32_t max_selected, n_first, n_last;
-  int32_t width, chunks;
+  int32_t smem_scores;  // blocks whose scores fit the shared memory of the launch (0: re-read them)
 };
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreChunk = 256;  // blocks of one CTA
+constexpr int kSelectThreads = 256;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectCluster = 8;   // most CTAs of a row
+constexpr int kSelectBins = 1024;
+constexpr int kSelectFine = 512;    // border blocks ranked in shared memory
+
+// Error bound of a 32-bit score over sum_d |q_d| times the largest |bound|.
+// 32-bit sums of 2 D = 256 products lose at most 256 x 2^-24 = 2^-16 of that.
+// Tensor cores align the 16 products and the sum of a step to the largest of
+// them and drop bits below 2^-23 of it: 17 x 2^-23 a step, 16 steps, 2^-14.9.
+constexpr float kScoreError = 1.0f / 16384;
 
 // Blocks of sequence b (0 for a length outside the table's capacity, which is
 // recorded).
@@ -227,6 +248,7 @@ __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b, bool record
   return (L + a.block_size - 1) / a.block_size;
 }
 
+// The tile (block, KV head) of logical block j.
 __device__ __forceinline__ int64_t bounds_tile(const SelectArgs& a, int b, int j, int g) {
   int phys = a.block_tables[static_cast<int64_t>(b) * a.max_blocks + j];
   if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.num_blocks)) {
@@ -242,7 +264,7 @@ struct QueryOf { using type = T; };
 template <>
 struct QueryOf<E4m3> { using type = __half; };
 
-// Element d of a bounds row as a float.
+// Element i of a bounds array as a float.
 template <typename T>
 __device__ __forceinline__ float bound_at(const void* base, int64_t i) {
   if constexpr (std::is_same_v<T, E4m3>) {
@@ -252,77 +274,6 @@ __device__ __forceinline__ float bound_at(const void* base, int64_t i) {
     return widen1<T>(static_cast<const T*>(base)[i]);
   }
 }
-
-// One warp per block, lanes over the channels.  Bytes bound it: 2 D elements
-// per block and KV head are read once for the G heads of the group.
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectArgs a) {
-  using Q = typename QueryOf<T>::type;
-  constexpr int kPer = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
-  const int b = row / a.num_kv_heads, g = row - b * a.num_kv_heads;
-  const int nblk = blocks_of(a, b, chunk == 0 && g == 0 && threadIdx.x == 0);
-  const int j0 = chunk * kScoreChunk;
-  if (nblk <= a.max_selected || j0 >= nblk) return;  // every block is selected, or none is here
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float neg[G][kPer], pos[G][kPer];
-#pragma unroll
-  for (int h = 0; h < G; ++h)
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float x = widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + h) * D + i * 32 + lane]);
-      neg[h][i] = x < 0.f ? x : (x == x ? 0.f : x);
-      pos[h][i] = x > 0.f ? x : (x == x ? 0.f : x);
-    }
-  float big = 0.f;
-  const int j1 = min(nblk, j0 + kScoreChunk);
-  for (int j = j0 + warp; j < j1; j += kScoreThreads / 32) {
-    const int64_t at = bounds_tile(a, b, j, g) * 2 * D + lane;
-    float s[G];
-#pragma unroll
-    for (int h = 0; h < G; ++h) s[h] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float lo = bound_at<T>(a.bounds, at + i * 32), hi = bound_at<T>(a.bounds, at + D + i * 32);
-      big = MinMax<float>::mx(big, MinMax<float>::mx(fabsf(lo), fabsf(hi)));
-#pragma unroll
-      for (int h = 0; h < G; ++h) s[h] += neg[h][i] * lo + pos[h][i] * hi;
-    }
-    float best = 0.f;
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s[h] += __shfl_xor_sync(kFull, s[h], o);
-      best = h ? MinMax<float>::mx(best, s[h]) : s[0];
-    }
-    if (lane == 0) a.scores[static_cast<int64_t>(row) * a.width + j] = best;
-  }
-  __shared__ float red[kScoreThreads / 32];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
-  if (lane == 0) red[warp] = big;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kScoreThreads / 32; ++w) big = MinMax<float>::mx(big, red[w]);
-    a.chunk_max[static_cast<int64_t>(row) * a.chunks + chunk] = big;
-  }
-}
-
-// ---------------------------------------------------------------------------
-// the selection: one CTA per (sequence, KV head)
-// ---------------------------------------------------------------------------
-constexpr int kSelectThreads = 512;
-constexpr int kSelectBins = 2048;
-constexpr int kSelectFine = 512;  // border blocks ranked in shared memory
-
-// Error bound of a 32-bit score over sum_d |q_d| times the largest |bound|.
-// The longest chain of sums is 2 D = 256 products: in 32-bit adds it loses at
-// most 256 x 2^-24 = 2^-16 of that.  Tensor cores align the 16 products and
-// the sum of a step to the largest of them and drop bits below 2^-23 of it:
-// 17 x 2^-23 a step, 16 steps, 2^-14.9.
-constexpr float kScoreError = 1.0f / 16384;
 
 // Order-preserving map of floats to unsigned integers; NaN above everything.
 __device__ __forceinline__ uint32_t key32(float x) {
@@ -341,170 +292,355 @@ __device__ __forceinline__ uint64_t key64(double x) {
   return u >> 63 ? ~u : u | (1ull << 63);
 }
 
-// The score of block j in 64 bits (all lanes of the warp get it).
-template <typename T, int D>
-__device__ __forceinline__ uint64_t fine_key(const SelectArgs& a, int b, int g, int G, int j) {
+// Scores of 16 blocks by one warp.  On the tensor cores the blocks are the 16
+// rows of A, the heads the 8 columns of B and the 2 D bound channels the
+// contraction, in an order of its own: each lane's 16-byte loads of a row are
+// its A fragments as they come (channels e0 + 4 s .. + 3 of piece i in step
+// s), and B is q in the same order, min(q, 0) against the minima and
+// max(q, 0) against the maxima.
+template <typename T, int D, int G>
+struct Scorer {
   using Q = typename QueryOf<T>::type;
-  const int lane = threadIdx.x & 31;
-  const int64_t at = bounds_tile(a, b, j, g) * 2 * D + lane;
-  double lo[D / 32], hi[D / 32];
+  using M = MinMax<Q>;
+  static constexpr int kElems = 16 / static_cast<int>(sizeof(T));  // of a load
+  static constexpr int kPieces = 2 * D / (4 * kElems);             // loads of a row by a lane
+  static constexpr int kSteps = kElems / 4;                        // mma steps of a piece
+  uint32_t q[kPieces][kSteps][2];
+  typename M::Reg big;
+
+  __device__ __forceinline__ void init(const SelectArgs& a, int b, int g) {
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    const typename M::Reg zero = M::as(0);
+    big = zero;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    lo[i] = bound_at<T>(a.bounds, at + i * 32);
-    hi[i] = bound_at<T>(a.bounds, at + D + i * 32);
-  }
-  uint64_t best = 0;
-#pragma unroll 1
-  for (int h = 0; h < G; ++h) {
-    double s = 0;
+    for (int i = 0; i < kPieces; ++i) {
+      const int e0 = i * 4 * kElems + tq * kElems, d0 = e0 % D;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const float x = widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + h) * D + i * 32 + lane]);
-      const double xn = x > 0.f ? 0.0 : x, xp = x < 0.f ? 0.0 : x;
-      s += xn * lo[i] + xp * hi[i];
+      for (int s = 0; s < kSteps; ++s) {
+        uint2 w = make_uint2(0, 0);
+        if (gq < G)
+          w = *reinterpret_cast<const uint2*>(static_cast<const Q*>(a.q) +
+                                              (static_cast<int64_t>(b) * a.num_q_heads + g * G + gq) * D + d0 + 4 * s);
+        const typename M::Reg x = M::as(w.x), y = M::as(w.y);
+        q[i][s][0] = M::bits(e0 < D ? M::mn(x, zero) : M::mx(x, zero));
+        q[i][s][1] = M::bits(e0 < D ? M::mn(y, zero) : M::mx(y, zero));
+      }
     }
+  }
+
+  // tile[2]: the tiles of rows lane / 4 and lane / 4 + 8.  Returns their
+  // scores (in all lanes of the row).
+  __device__ __forceinline__ float2 score(const SelectArgs& a, const int64_t (&tile)[2]) {
+    const int lane = threadIdx.x & 31, tq = lane & 3;
+    uint4 x[2][kPieces];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    const uint64_t k = key64(s);
+    for (int r = 0; r < 2; ++r) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.bounds) + tile[r] * 2 * D) + tq;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) x[r][i] = __ldg(src + 4 * i);
+    }
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      uint32_t w[2][2 * kSteps];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t v[4] = {x[r][i].x, x[r][i].y, x[r][i].z, x[r][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (sizeof(T) == 1) {
+            w[r][2 * k] = e4m3x2_to_f16x2(v[k]);
+            w[r][2 * k + 1] = e4m3x2_to_f16x2(v[k] >> 16);
+          } else {
+            w[r][k] = v[k];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2 * kSteps; ++k) big = M::mx(big, __habs2(M::as(w[r][k])));
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const uint32_t f[4] = {w[0][2 * s], w[1][2 * s], w[0][2 * s + 1], w[1][2 * s + 1]};
+        mma_16816<Q>(c, f, q[i][s][0], q[i][s][1]);
+      }
+    }
+    using F = MinMax<float>;
+    const bool h0 = 2 * tq < G, h1 = 2 * tq + 1 < G;
+    float2 s = make_float2(h0 ? c[0] : -INFINITY, h0 ? c[2] : -INFINITY);
+    if (h1) s = make_float2(F::mx(s.x, c[1]), F::mx(s.y, c[3]));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      s.x = F::mx(s.x, __shfl_xor_sync(kFull, s.x, o));
+      s.y = F::mx(s.y, __shfl_xor_sync(kFull, s.y, o));
+    }
+    return s;
+  }
+
+  __device__ __forceinline__ float largest() const {
+    const uint32_t w = M::bits(big);
+    const Chunk<Q, 2> c = [&] { Chunk<Q, 2> t; t.raw = w; return t; }();
+    return MinMax<float>::mx(widen1<Q>(c.e[0]), widen1<Q>(c.e[1]));
+  }
+};
+
+// 32-bit bounds on the CUDA cores: lanes over the channels, four blocks at a
+// time; the result layout is that of the tensor-core form.
+template <int D, int G>
+struct Scorer<float, D, G> {
+  static constexpr int kPieces = 2 * D / 128;
+  float4 q[G][kPieces];
+  float big;
+
+  __device__ __forceinline__ void init(const SelectArgs& a, int b, int g) {
+    using F = MinMax<float>;
+    const int lane = threadIdx.x & 31;
+    big = 0.f;
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int e0 = i * 128 + lane * 4;
+        const float4 x = *reinterpret_cast<const float4*>(
+            static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + g * G + h) * D + e0 % D);
+        q[h][i] = e0 < D ? make_float4(F::mn(x.x, 0.f), F::mn(x.y, 0.f), F::mn(x.z, 0.f), F::mn(x.w, 0.f))
+                         : make_float4(F::mx(x.x, 0.f), F::mx(x.y, 0.f), F::mx(x.z, 0.f), F::mx(x.w, 0.f));
+      }
+  }
+
+  __device__ __forceinline__ float2 score(const SelectArgs& a, const int64_t (&tile)[2]) {
+    using F = MinMax<float>;
+    const int lane = threadIdx.x & 31, gq = lane >> 2;
+    float2 out = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int r0 = 0; r0 < 16; r0 += 4) {
+      float4 x[4][kPieces];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // row r0 + r lies with lane 4 (row mod 8), in tile[row / 8]
+        const int64_t t = __shfl_sync(kFull, r0 < 8 ? tile[0] : tile[1], 4 * ((r0 + r) & 7));
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.bounds) + t * 2 * D) + lane;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) x[r][i] = __ldg(src + 32 * i);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float best = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          big = F::mx(big, F::mx(F::mx(fabsf(x[r][i].x), fabsf(x[r][i].y)), F::mx(fabsf(x[r][i].z), fabsf(x[r][i].w))));
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          float s = 0.f;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i)
+            s += q[h][i].x * x[r][i].x + q[h][i].y * x[r][i].y + q[h][i].z * x[r][i].z + q[h][i].w * x[r][i].w;
+#pragma unroll
+          for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+          best = h ? F::mx(best, s) : s;
+        }
+        if (gq == ((r0 + r) & 7)) {
+          if (r0 < 8) out.x = best;
+          else out.y = best;
+        }
+      }
+    }
+    return out;
+  }
+
+  __device__ __forceinline__ float largest() const { return big; }
+};
+
+// The score of block j in 64 bits (all lanes of the warp get its key).
+template <typename T, int D, int G>
+__device__ __forceinline__ uint64_t fine_key(const SelectArgs& a, int b, int g, int j) {
+  using Q = typename QueryOf<T>::type;
+  constexpr int kPer = D / 32;  // a lane's channels, adjacent
+  const int d0 = (threadIdx.x & 31) * kPer;
+  const int64_t at = bounds_tile(a, b, j, g) * 2 * D + d0;
+  double lo[kPer], hi[kPer], s[G];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    lo[i] = bound_at<T>(a.bounds, at + i);
+    hi[i] = bound_at<T>(a.bounds, at + D + i);
+  }
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    s[h] = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float x = widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + h) * D + d0 + i]);
+      const double xn = x > 0.f ? 0.0 : x, xp = x < 0.f ? 0.0 : x;
+      s[h] += xn * lo[i] + xp * hi[i];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int h = 0; h < G; ++h) s[h] += __shfl_xor_sync(kFull, s[h], o);
+  uint64_t best = 0;
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    const uint64_t k = key64(s[h]);
     best = k > best ? k : best;
   }
   return best;
 }
 
-// Block-wide sum of one value per thread; `red` holds a word per warp.
-__device__ __forceinline__ int block_sum(int x, int* red) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  int s = 0;
-  for (int w = 0; w < kSelectThreads / 32; ++w) s += red[w];
-  return s;
-}
-
-// Finds in hist[0 .. bins) (counts per bin, larger keys in higher bins) the
-// bin in which the need-th largest lies: returns it, and in *above the count
-// in higher bins.
-__device__ __forceinline__ int find_bin(const int* hist, int bins, int need, int* above, int* red, int* shared2) {
-  // thread t owns bins - 1 - t * per ... downwards
-  const int per = (bins + kSelectThreads - 1) / kSelectThreads;
-  int mine = 0;
-  const int top = bins - 1 - static_cast<int>(threadIdx.x) * per;
-  for (int i = 0; i < per; ++i)
-    if (top - i >= 0) mine += hist[top - i];
-  int before = mine;  // inclusive prefix over the warp
+// Finds in hist[0 .. bins) (counts per bin, larger keys in higher bins; bins a
+// multiple of the threads) the bin in which the need-th largest lies; *above:
+// the count in higher bins.  One count must reach `need`.
+__device__ __forceinline__ int find_bin(const int* hist, int bins, int need, int* above, int* red, int* two) {
+  const int per = bins / kSelectThreads;
+  const int top = bins - 1 - static_cast<int>(threadIdx.x) * per;  // this thread's highest bin
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int mine = 0;
+  for (int i = 0; i < per; ++i) mine += hist[top - i];
+  int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(kFull, before, o);
     if (lane >= o) before += y;
   }
-  __syncthreads();
   if (lane == 31) red[warp] = before;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) before += red[w];
-  before -= mine;  // exclusive
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w)
+    if (w < warp) before += red[w];
+  before -= mine;
   if (before < need && before + mine >= need) {
-    int run = before;
-    for (int i = 0; i < per; ++i) {
-      const int k = top - i;
-      if (k < 0) break;
-      if (run + hist[k] >= need) {
-        shared2[0] = k;
-        shared2[1] = run;
-        break;
-      }
-      run += hist[k];
-    }
+    int run = before, i = 0;
+    while (i < per - 1 && run + hist[top - i] < need) run += hist[top - i++];
+    two[0] = top - i;
+    two[1] = run;
   }
   __syncthreads();
-  *above = shared2[1];
-  return shared2[0];
+  *above = two[1];
+  return two[0];
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs a) {
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectArgs a) {
   using Q = typename QueryOf<T>::type;
-  extern __shared__ uint32_t bitmap[];  // one bit per block
+  extern __shared__ uint32_t bitmap[];  // one bit per block, then the scores of up to smem_scores blocks
   __shared__ int hist[kSelectBins];
   __shared__ uint64_t fine[kSelectFine];
   __shared__ int fine_at[kSelectFine];
-  __shared__ int red[kSelectThreads / 32], two[2], count;
-  __shared__ uint32_t range[2];
-  __shared__ float eps_s;
+  __shared__ int red[kSelectWarps], two[2], count[2];
+  __shared__ SelectStats warp_stats[kSelectWarps];
+  __shared__ float q_norm[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int g = blockIdx.x % a.num_kv_heads, b = blockIdx.x / a.num_kv_heads;
-  const int G = a.num_q_heads / a.num_kv_heads;
+  uint32_t rank, ctas;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int64_t row = blockIdx.x / ctas;
+  const int b = static_cast<int>(row / a.num_kv_heads), g = static_cast<int>(row - static_cast<int64_t>(b) * a.num_kv_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t row = blockIdx.x;
-  const int nblk = blocks_of(a, b, false);
+  const int nblk = blocks_of(a, b, rank == 0 && g == 0 && tid == 0);
   const int K = a.max_selected;
   int32_t* out = a.selected + row * K;
-  if (nblk <= K) {
-    for (int i = tid; i < K; i += kSelectThreads) out[i] = i < nblk ? i : -1;
+  if (nblk <= K) {  // every block
+    if (rank == 0)
+      for (int i = tid; i < K; i += kSelectThreads) out[i] = i < nblk ? i : -1;
     return;
   }
-  const int c0 = a.n_first, c1 = nblk - a.n_last;  // candidates [c0, c1): more than are needed, since nblk > K
+  const int c0 = a.n_first, c1 = nblk - a.n_last;  // the candidates: more than are needed, since nblk > K
   const int need0 = K - a.n_first - a.n_last;
-  const int words = (nblk + 31) / 32;
-  for (int i = tid; i < words; i += kSelectThreads) {
-    uint32_t m = 0;
-    for (int t = 0; t < 32; ++t) {
-      const int j = i * 32 + t;
-      if (j < nblk && (j < c0 || j >= c1)) m |= 1u << t;
-    }
-    bitmap[i] = m;
-  }
-  const float* scores = a.scores + row * a.width;
+  float* row_scores = a.scores + row * a.max_blocks;
+  SelectStats* row_stats = a.stats + row * kSelectCluster;
 
   if (need0 > 0) {
-    // ---- the error bound of this row's scores ----
-    if (warp == 0) {
-      float q1 = 0.f;
-      for (int h = 0; h < G; ++h) {
-        float s = 0.f;
-        for (int d = lane; d < D; d += 32)
-          s += fabsf(widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + h) * D + d]));
+    // ---- 32-bit scores of this CTA's slice ----
+    const int tiles = (nblk + 15) / 16;
+    const int per = (tiles + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
+    const int t1 = min(tiles, (static_cast<int>(rank) + 1) * per);
+    Scorer<T, D, G> scorer;
+    scorer.init(a, b, g);
+    uint32_t mn = 0xffffffffu, mx = 0;
+    for (int t = static_cast<int>(rank) * per + warp; t < t1; t += kSelectWarps) {
+      const int gq = lane >> 2;
+      int64_t tile[2];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-        q1 = MinMax<float>::mx(q1, s);
+      for (int r = 0; r < 2; ++r) tile[r] = bounds_tile(a, b, min(t * 16 + gq + 8 * r, nblk - 1), g);
+      const float2 s = scorer.score(a, tile);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int j = t * 16 + gq + 8 * r;
+        const float x = r ? s.y : s.x;
+        if ((lane & 3) == 0 && j < nblk) row_scores[j] = x;
+        if (j >= c0 && j < c1) {
+          const uint32_t k = key32(x);
+          mn = min(mn, k);
+          mx = max(mx, k);
+        }
       }
-      float big = 0.f;
-      for (int i = lane; i < (nblk + kScoreChunk - 1) / kScoreChunk; i += 32)
-        big = MinMax<float>::mx(big, a.chunk_max[row * a.chunks + i]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
-      if (lane == 0) eps_s = q1 * big * kScoreError;
     }
-    if (tid == 0) {
-      range[0] = 0xffffffffu;
-      range[1] = 0;
+    float big = scorer.largest();
+#pragma unroll
+    for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
+    mn = __reduce_min_sync(kFull, mn);
+    mx = __reduce_max_sync(kFull, mx);
+    if (lane == 0) warp_stats[warp] = SelectStats{mn, mx, big, 0.f};
+    if (rank == 0 && warp < G) {  // sum |q| of each head, for the error bound
+      float s = 0.f;
+      for (int d = lane; d < D; d += 32)
+        s += fabsf(widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + warp) * D + d]));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+      if (lane == 0) q_norm[warp] = s;
     }
     __syncthreads();
-    const float eps = eps_s;
+    if (tid == 0) {
+      SelectStats st = warp_stats[0];
+      for (int w = 1; w < kSelectWarps; ++w) {
+        st.min_key = min(st.min_key, warp_stats[w].min_key);
+        st.max_key = max(st.max_key, warp_stats[w].max_key);
+        st.big = MinMax<float>::mx(st.big, warp_stats[w].big);
+      }
+      row_stats[rank] = st;
+    }
+    // every CTA's scores and statistics are in the workspace
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else if (rank != 0) {
+    return;
+  }
+
+  const int words = (nblk + 31) / 32;
+  for (int i = tid; i < words; i += kSelectThreads) {  // the first and the last blocks
+    uint32_t m = 0;
+    if (i * 32 < c0) m |= c0 - i * 32 >= 32 ? kFull : (1u << (c0 - i * 32)) - 1;
+    if (i * 32 + 32 > c1) m |= c1 <= i * 32 ? kFull : kFull << (c1 - i * 32);
+    if (i == words - 1 && (nblk & 31)) m &= (1u << (nblk & 31)) - 1;
+    bitmap[i] = m;
+  }
+
+  if (need0 > 0) {
+    const float* scores = row_scores;
+    if (nblk <= a.smem_scores) {
+      float* copy = reinterpret_cast<float*>(bitmap + (a.max_blocks + 31) / 32);
+      for (int j = tid; j < nblk; j += kSelectThreads) copy[j] = row_scores[j];
+      scores = copy;
+    }
+    uint32_t base = 0xffffffffu, last = 0;
+    float big = 0.f, q1 = 0.f;
+    for (uint32_t r = 0; r < ctas; ++r) {
+      const SelectStats st = row_stats[r];
+      base = min(base, st.min_key);
+      last = max(last, st.max_key);
+      big = MinMax<float>::mx(big, st.big);
+    }
+#pragma unroll
+    for (int h = 0; h < G; ++h) q1 = MinMax<float>::mx(q1, q_norm[h]);
+    const float eps = q1 * big * kScoreError;
     const bool bounded = eps <= 1e30f;  // false for infinities and NaN: every candidate is scored in 64 bits
 
     // ---- narrow the keys' range to a bin that holds the need0-th largest ----
     float t_lo = -INFINITY, t_hi = INFINITY;  // the need0-th largest score lies in [t_lo, t_hi]
     if (bounded) {
-      uint32_t mn = 0xffffffffu, mx = 0;
-      for (int j = c0 + tid; j < c1; j += kSelectThreads) {
-        const uint32_t k = key32(scores[j]);
-        mn = min(mn, k);
-        mx = max(mx, k);
-      }
-      mn = __reduce_min_sync(kFull, mn);
-      mx = __reduce_max_sync(kFull, mx);
-      if (lane == 0) {
-        atomicMin(&range[0], mn);
-        atomicMax(&range[1], mx);
-      }
-      __syncthreads();
-      uint32_t base = range[0], last = range[1];
       int need = need0;
-      for (;;) {
+      for (;;) {  // each round keeps less than 1 / 512 of the range
         int shift = 0;
         while (((last - base) >> shift) >= kSelectBins) ++shift;
         for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
@@ -518,25 +654,24 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs
         const int bin = find_bin(hist, kSelectBins, need, &above, red, two);
         const int in_bin = hist[bin];
         need -= above;
-        const uint32_t nb = base + (static_cast<uint32_t>(bin) << shift);
-        const uint32_t width = shift ? (1u << shift) - 1 : 0;
-        last = last - nb < width ? last : nb + width;
-        base = nb;
+        base += static_cast<uint32_t>(bin) << shift;
+        const uint32_t width = (1u << shift) - 1;
+        if (last - base > width) last = base + width;
         __syncthreads();
-        if (shift == 0 || in_bin <= 32) break;
+        if (shift == 0 || in_bin <= 8) break;
       }
       t_lo = unkey32(base);
       t_hi = unkey32(last);
     }
 
     // ---- blocks surely in, and those near the border ----
-    // exact scores are within eps of these: above t_hi + 2 eps a block beats
-    // the border, below t_lo - 2 eps it does not reach it
+    // A 64-bit score is within eps of its 32-bit one.  Fewer than need0 blocks
+    // score above t_hi, so the need0-th largest 64-bit score is at most
+    // t_hi + eps, and likewise at least t_lo - eps.
     const float in_above = bounded ? t_hi + 2.f * eps : INFINITY;
     const float out_below = bounded ? t_lo - 2.f * eps : -INFINITY;
-    if (tid == 0) count = 0;
+    if (tid < 2) count[tid] = 0;
     __syncthreads();
-    int sure = 0;
     for (int j0 = 0; j0 < words * 32; j0 += kSelectThreads) {
       const int j = j0 + tid;
       bool in = false, near = false;
@@ -546,48 +681,50 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs
         near = !in && !(bounded && s < out_below);
       }
       const uint32_t m = __ballot_sync(kFull, in);
-      if (lane == 0 && m) bitmap[j >> 5] |= m;
-      sure += in;
+      if (lane == 0 && m) {
+        bitmap[j >> 5] |= m;
+        atomicAdd(&count[1], __popc(m));
+      }
       if (near) {
-        const int at = atomicAdd(&count, 1);
+        const int at = atomicAdd(&count[0], 1);
         if (at < kSelectFine) fine_at[at] = j;
       }
     }
-    sure = block_sum(sure, red);
-    const int n_near = count;
-    const int need = need0 - sure;  // of the near blocks
+    __syncthreads();
+    const int n_near = count[0], need = need0 - count[1];  // of the near blocks
 
     if (n_near <= kSelectFine) {
-      for (int i = warp; i < n_near; i += kSelectThreads / 32) {
-        const uint64_t k = fine_key<T, D>(a, b, g, G, fine_at[i]);
-        if (lane == 0) fine[i] = k;
+      if (n_near > need) {
+        for (int i = warp; i < n_near; i += kSelectWarps) {
+          const uint64_t k = fine_key<T, D, G>(a, b, g, fine_at[i]);
+          if (lane == 0) fine[i] = k;
+        }
+        __syncthreads();
       }
-      __syncthreads();
       for (int i = tid; i < n_near; i += kSelectThreads) {
-        const uint64_t k = fine[i];
         const int j = fine_at[i];
-        int rank = 0;
-        for (int x = 0; x < n_near; ++x) rank += fine[x] > k || (fine[x] == k && fine_at[x] < j);
-        if (rank < need) atomicOr(&bitmap[j >> 5], 1u << (j & 31));
+        int rank_of = 0;
+        if (n_near > need) {
+          const uint64_t k = fine[i];
+          for (int x = 0; x < n_near; ++x) rank_of += fine[x] > k || (fine[x] == k && fine_at[x] < j);
+        }
+        if (rank_of < need) atomicOr(&bitmap[j >> 5], 1u << (j & 31));
       }
     } else {
       // many blocks within the error of the border (equal keys, infinities):
-      // 64-bit keys in global memory and a radix selection over them
-      uint64_t* keys = reinterpret_cast<uint64_t*>(a.fine + row * a.width);
-      for (int j = c0 + warp; j < c1; j += kSelectThreads / 32) {
+      // 64-bit keys in the workspace and a radix selection over them
+      uint64_t* keys = a.fine + row * a.max_blocks;
+      for (int j = c0 + warp; j < c1; j += kSelectWarps) {
         const float s = scores[j];
-        const bool in = bounded && s > in_above;
-        const bool near = !in && !(bounded && s < out_below);
-        if (near) {
-          const uint64_t k = fine_key<T, D>(a, b, g, G, j);
-          if (lane == 0) keys[j] = k;
-        }
+        if (bounded && (s > in_above || s < out_below)) continue;
+        const uint64_t k = fine_key<T, D, G>(a, b, g, j);
+        if (lane == 0) keys[j] = k;
       }
       __syncthreads();
       uint64_t prefix = 0;
       int left = need;
       for (int shift = 56; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
+        hist[tid] = 0;  // 256 bins
         __syncthreads();
         for (int j = c0 + tid; j < c1; j += kSelectThreads) {
           const float s = scores[j];
@@ -619,7 +756,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs
         if (lane == 0) red[warp] = __popc(me);
         __syncthreads();
         int before = equal + __popc(me & ((1u << lane) - 1));
-        for (int w = 0; w < kSelectThreads / 32; ++w) {
+#pragma unroll
+        for (int w = 0; w < kSelectWarps; ++w) {
           if (w < warp) before += red[w];
           equal += red[w];
         }
@@ -646,7 +784,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs
     if (lane == 31) red[warp] = at;
     __syncthreads();
     at += done - n;
-    for (int x = 0; x < kSelectThreads / 32; ++x) {
+#pragma unroll
+    for (int x = 0; x < kSelectWarps; ++x) {
       if (x < warp) at += red[x];
       done += red[x];
     }

@@ -39,42 +39,69 @@ cudaError_t launch_bounds(const pkv::BoundsArgs& a, cudaStream_t s) {
 }
 
 struct SelectLayout {
-  int32_t chunks;
-  size_t chunk_max, fine, total;  // byte offsets; the scores lie at 0
+  size_t stats, fine, total;  // byte offsets; the scores lie at 0
 };
 
 SelectLayout select_layout(int64_t rows, int64_t max_blocks) {
   SelectLayout w;
-  w.chunks = static_cast<int32_t>((max_blocks + pkv::kScoreChunk - 1) / pkv::kScoreChunk);
-  w.chunk_max = round256(static_cast<size_t>(rows * max_blocks) * sizeof(float));
-  w.fine = w.chunk_max + round256(static_cast<size_t>(rows * w.chunks) * sizeof(float));
-  w.total = w.fine + round256(static_cast<size_t>(rows * max_blocks) * sizeof(double));
+  w.stats = round256(static_cast<size_t>(rows * max_blocks) * sizeof(float));
+  w.fine = w.stats + round256(static_cast<size_t>(rows) * pkv::kSelectCluster * sizeof(pkv::SelectStats));
+  w.total = w.fine + round256(static_cast<size_t>(rows * max_blocks) * sizeof(uint64_t));
   return w;
 }
 
-template <typename T, int D>
-int launch_select(const pkv::SelectArgs& a, const char* fn, cudaStream_t s) {
-  const unsigned rows = static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.num_kv_heads);
-  cudaError_t e = cudaSuccess;
-  if (a.width > a.max_selected) {  // else no sequence has blocks to choose from
-    const dim3 grid(rows * static_cast<unsigned>(a.chunks)), block(pkv::kScoreThreads);
-    switch (a.num_q_heads / a.num_kv_heads) {
-      case 1: e = launch_pdl(pkv::score_kernel<T, D, 1>, grid, block, 0, s, a); break;
-      case 2: e = launch_pdl(pkv::score_kernel<T, D, 2>, grid, block, 0, s, a); break;
-      case 4: e = launch_pdl(pkv::score_kernel<T, D, 4>, grid, block, 0, s, a); break;
-      default: e = launch_pdl(pkv::score_kernel<T, D, 8>, grid, block, 0, s, a);
-    }
-    if (e != cudaSuccess) return cuda_fail(e, fn);
-  }
-  const size_t smem = static_cast<size_t>((a.width + 31) / 32) * 4;
-  if (smem > 16 * 1024) {
-    e = cudaFuncSetAttribute(pkv::select_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kMaxSelectBlocks / 8));
+// Shared memory of a selecting CTA: the bitmap, and a copy of the scores where
+// it leaves room for two CTAs on an SM.
+constexpr int32_t kSelectSmemScores = 16384;
+
+template <typename T, int D, int G>
+int launch_select(pkv::SelectArgs a, const char* fn, cudaStream_t s) {
+  auto kern = pkv::select_kernel<T, D, G>;
+  const int64_t rows = int64_t(a.num_seqs) * a.num_kv_heads;
+  // CTAs of a row: as many as keep the row's tiles of 16 blocks two to a warp
+  // and the grid within three rounds of two CTAs an SM
+  int ctas = 1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int64_t tiles = (int64_t(a.max_blocks) + 15) / 16;
+  while (ctas < pkv::kSelectCluster && rows * ctas * 2 <= 6 * int64_t(sm_count(dev)) &&
+         tiles > int64_t(2) * ctas * pkv::kSelectWarps)
+    ctas *= 2;
+  a.smem_scores = a.max_blocks <= kSelectSmemScores ? a.max_blocks : 0;
+  const size_t smem = static_cast<size_t>((a.max_blocks + 31) / 32 + a.smem_scores) * 4;
+  static std::atomic<bool> opted[kMaxDevices];
+  if (dev >= kMaxDevices || !opted[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSelectBlocks / 8));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select)");
+    if (dev < kMaxDevices) opted[dev].store(true, std::memory_order_relaxed);
   }
-  e = launch_pdl(pkv::select_kernel<T, D>, dim3(rows), dim3(pkv::kSelectThreads), smem, s, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
+  cfg.blockDim = dim3(pkv::kSelectThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return pkv::ok();
+}
+
+template <typename T, int D>
+int launch_select_group(const pkv::SelectArgs& a, const char* fn, cudaStream_t s) {
+  switch (a.num_q_heads / a.num_kv_heads) {
+    case 1: return launch_select<T, D, 1>(a, fn, s);
+    case 2: return launch_select<T, D, 2>(a, fn, s);
+    case 4: return launch_select<T, D, 4>(a, fn, s);
+    default: return launch_select<T, D, 8>(a, fn, s);
+  }
 }
 
 struct SparseLayout {
@@ -216,7 +243,6 @@ extern "C" int pkv_block_select(const void* q, const void* bounds, const int32_t
   const SelectLayout w = select_layout(rows, max_blocks_per_seq);
   if (workspace_bytes < w.total)
     return fail(PKV_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, w.total);
-  if (rows * w.chunks > INT32_MAX) return fail(PKV_ERR_INVALID_ARG, "%s: too many blocks in one call", fn);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   pkv::SelectArgs a{};
   a.q = q;
@@ -224,8 +250,8 @@ extern "C" int pkv_block_select(const void* q, const void* bounds, const int32_t
   a.block_tables = block_tables;
   a.seq_lens = seq_lens;
   a.scores = reinterpret_cast<float*>(ws);
-  a.chunk_max = reinterpret_cast<float*>(ws + w.chunk_max);
-  a.fine = reinterpret_cast<double*>(ws + w.fine);
+  a.stats = reinterpret_cast<pkv::SelectStats*>(ws + w.stats);
+  a.fine = reinterpret_cast<uint64_t*>(ws + w.fine);
   a.selected = selected;
   a.num_seqs = num_seqs;
   a.num_q_heads = num_q_heads;
@@ -236,15 +262,13 @@ extern "C" int pkv_block_select(const void* q, const void* bounds, const int32_t
   a.max_selected = max_selected;
   a.n_first = n_first;
   a.n_last = n_last;
-  a.width = max_blocks_per_seq;
-  a.chunks = w.chunks;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool d128 = head_dim == 128;
   switch (dtype) {
-    case PKV_F32: return d128 ? launch_select<float, 128>(a, fn, s) : launch_select<float, 64>(a, fn, s);
-    case PKV_BF16: return d128 ? launch_select<__nv_bfloat16, 128>(a, fn, s) : launch_select<__nv_bfloat16, 64>(a, fn, s);
-    case PKV_F16: return d128 ? launch_select<__half, 128>(a, fn, s) : launch_select<__half, 64>(a, fn, s);
-    default: return launch_select<pkv::E4m3, 128>(a, fn, s);
+    case PKV_F32: return d128 ? launch_select_group<float, 128>(a, fn, s) : launch_select_group<float, 64>(a, fn, s);
+    case PKV_BF16: return d128 ? launch_select_group<__nv_bfloat16, 128>(a, fn, s) : launch_select_group<__nv_bfloat16, 64>(a, fn, s);
+    case PKV_F16: return d128 ? launch_select_group<__half, 128>(a, fn, s) : launch_select_group<__half, 64>(a, fn, s);
+    default: return launch_select_group<pkv::E4m3, 128>(a, fn, s);
   }
 }
 
