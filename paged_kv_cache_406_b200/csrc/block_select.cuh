@@ -197,16 +197,11 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// selection: a cluster of CTAs per (sequence, KV head)
-//
-// Bytes bound the scoring: 2 D elements per block and KV head, read once for
-// the G heads of the group.  The CTAs of a cluster take equal slices of the
-// row's blocks, 16 blocks a warp at a time, and write 32-bit scores to the
-// workspace; rank 0 then selects (the others leave), so that the selection
-// of one row runs under the scoring of others and needs no launch of its own.
+// selection: score_kernel, then select_kernel with one CTA per (sequence, KV
+// head).
 // ---------------------------------------------------------------------------
-struct SelectStats {  // of one CTA's scores
-  uint32_t min_key, max_key;  // candidates' keys
+struct TileStats {  // of 16 scores
+  uint32_t min_key, max_key;  // the candidates' keys
   float big;                  // largest |bound|
   float pad;
 };
@@ -217,17 +212,17 @@ struct SelectArgs {
   const int32_t* block_tables;
   const int32_t* seq_lens;
   float* scores;       // [num_seqs * num_kv_heads][max_blocks]
-  SelectStats* stats;  // [num_seqs * num_kv_heads][kSelectCluster]
+  TileStats* stats;    // [num_seqs * num_kv_heads][tiles]
   uint64_t* fine;      // [num_seqs * num_kv_heads][max_blocks]: 64-bit keys, where there are too many for shared memory
   int32_t* selected;   // [num_seqs][num_kv_heads][max_selected]
   int32_t num_seqs, num_q_heads, num_kv_heads, num_blocks, max_blocks, block_size;
   int32_t max_selected, n_first, n_last;
+  int32_t tiles;        // of 16 blocks, in max_blocks
   int32_t smem_scores;  // blocks whose scores fit the shared memory of the launch (0: re-read them)
 };
 
-constexpr int kSelectThreads = 256;
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectCluster = 8;   // most CTAs of a row
 constexpr int kSelectBins = 1024;
 constexpr int kSelectFine = 512;    // border blocks ranked in shared memory
 
@@ -248,9 +243,8 @@ __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b, bool record
   return (L + a.block_size - 1) / a.block_size;
 }
 
-// The tile (block, KV head) of logical block j.
-__device__ __forceinline__ int64_t bounds_tile(const SelectArgs& a, int b, int j, int g) {
-  int phys = a.block_tables[static_cast<int64_t>(b) * a.max_blocks + j];
+// The tile (block, KV head) of a table entry.
+__device__ __forceinline__ int64_t bounds_tile(const SelectArgs& a, int phys, int g) {
   if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.num_blocks)) {
     record_error(PKV_ERR_BAD_BLOCK);
     phys = 0;
@@ -306,12 +300,12 @@ struct Scorer {
   static constexpr int kPieces = 2 * D / (4 * kElems);             // loads of a row by a lane
   static constexpr int kSteps = kElems / 4;                        // mma steps of a piece
   uint32_t q[kPieces][kSteps][2];
-  typename M::Reg big;
+  uint4 x[2][kPieces];  // the tile's rows lane / 4 and lane / 4 + 8
+  typename M::Reg big[4];
 
-  __device__ __forceinline__ void init(const SelectArgs& a, int b, int g) {
+  __device__ __forceinline__ void group(const SelectArgs& a, int b, int g) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     const typename M::Reg zero = M::as(0);
-    big = zero;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int e0 = i * 4 * kElems + tq * kElems, d0 = e0 % D;
@@ -321,25 +315,31 @@ struct Scorer {
         if (gq < G)
           w = *reinterpret_cast<const uint2*>(static_cast<const Q*>(a.q) +
                                               (static_cast<int64_t>(b) * a.num_q_heads + g * G + gq) * D + d0 + 4 * s);
-        const typename M::Reg x = M::as(w.x), y = M::as(w.y);
-        q[i][s][0] = M::bits(e0 < D ? M::mn(x, zero) : M::mx(x, zero));
-        q[i][s][1] = M::bits(e0 < D ? M::mn(y, zero) : M::mx(y, zero));
+        const typename M::Reg y0 = M::as(w.x), y1 = M::as(w.y);
+        q[i][s][0] = M::bits(i < kPieces / 2 ? M::mn(y0, zero) : M::mx(y0, zero));
+        q[i][s][1] = M::bits(i < kPieces / 2 ? M::mn(y1, zero) : M::mx(y1, zero));
       }
     }
   }
 
-  // tile[2]: the tiles of rows lane / 4 and lane / 4 + 8.  Returns their
-  // scores (in all lanes of the row).
-  __device__ __forceinline__ float2 score(const SelectArgs& a, const int64_t (&tile)[2]) {
-    const int lane = threadIdx.x & 31, tq = lane & 3;
-    uint4 x[2][kPieces];
+  // tile[r]: of row lane / 4 + 8 r
+  __device__ __forceinline__ void load(const SelectArgs& a, const int64_t (&tile)[2]) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.bounds) + tile[r] * 2 * D) + tq;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.bounds) + tile[r] * 2 * D) + (threadIdx.x & 3);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) x[r][i] = __ldg(src + 4 * i);
     }
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
+  }
+
+  // The scores of the two rows (in all four lanes of a row), and the largest
+  // |bound| this lane has met in the tile.
+  __device__ __forceinline__ float2 score(float* largest) {
+    const int tq = threadIdx.x & 3;
+    // four chains for the maxima and two for the sums: one would wait for itself
+    float c[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) big[k] = M::as(0);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       uint32_t w[2][2 * kSteps];
@@ -356,99 +356,221 @@ struct Scorer {
           }
         }
 #pragma unroll
-        for (int k = 0; k < 2 * kSteps; ++k) big = M::mx(big, __habs2(M::as(w[r][k])));
+        for (int k = 0; k < 2 * kSteps; ++k) big[k & 3] = M::mx(big[k & 3], __habs2(M::as(w[r][k])));
       }
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const uint32_t f[4] = {w[0][2 * s], w[1][2 * s], w[0][2 * s + 1], w[1][2 * s + 1]};
-        mma_16816<Q>(c, f, q[i][s][0], q[i][s][1]);
+        mma_16816<Q>(c[s & 1], f, q[i][s][0], q[i][s][1]);
       }
     }
     using F = MinMax<float>;
     const bool h0 = 2 * tq < G, h1 = 2 * tq + 1 < G;
-    float2 s = make_float2(h0 ? c[0] : -INFINITY, h0 ? c[2] : -INFINITY);
-    if (h1) s = make_float2(F::mx(s.x, c[1]), F::mx(s.y, c[3]));
+    float2 s = make_float2(h0 ? c[0][0] + c[1][0] : -INFINITY, h0 ? c[0][2] + c[1][2] : -INFINITY);
+    if (h1) s = make_float2(F::mx(s.x, c[0][1] + c[1][1]), F::mx(s.y, c[0][3] + c[1][3]));
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       s.x = F::mx(s.x, __shfl_xor_sync(kFull, s.x, o));
       s.y = F::mx(s.y, __shfl_xor_sync(kFull, s.y, o));
     }
+    Chunk<Q, 2> m;
+    m.raw = M::bits(M::mx(M::mx(big[0], big[1]), M::mx(big[2], big[3])));
+    *largest = F::mx(widen1<Q>(m.e[0]), widen1<Q>(m.e[1]));
     return s;
-  }
-
-  __device__ __forceinline__ float largest() const {
-    const uint32_t w = M::bits(big);
-    const Chunk<Q, 2> c = [&] { Chunk<Q, 2> t; t.raw = w; return t; }();
-    return MinMax<float>::mx(widen1<Q>(c.e[0]), widen1<Q>(c.e[1]));
   }
 };
 
 // 32-bit bounds on the CUDA cores: lanes over the channels, four blocks at a
-// time; the result layout is that of the tensor-core form.
+// time.
 template <int D, int G>
 struct Scorer<float, D, G> {
   static constexpr int kPieces = 2 * D / 128;
   float4 q[G][kPieces];
-  float big;
+  int64_t now[2];
+  const float* bounds;
 
-  __device__ __forceinline__ void init(const SelectArgs& a, int b, int g) {
+  __device__ __forceinline__ void group(const SelectArgs& a, int b, int g) {
     using F = MinMax<float>;
     const int lane = threadIdx.x & 31;
-    big = 0.f;
 #pragma unroll
     for (int h = 0; h < G; ++h)
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int e0 = i * 128 + lane * 4;
-        const float4 x = *reinterpret_cast<const float4*>(
+        const float4 y = *reinterpret_cast<const float4*>(
             static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + g * G + h) * D + e0 % D);
-        q[h][i] = e0 < D ? make_float4(F::mn(x.x, 0.f), F::mn(x.y, 0.f), F::mn(x.z, 0.f), F::mn(x.w, 0.f))
-                         : make_float4(F::mx(x.x, 0.f), F::mx(x.y, 0.f), F::mx(x.z, 0.f), F::mx(x.w, 0.f));
+        q[h][i] = e0 < D ? make_float4(F::mn(y.x, 0.f), F::mn(y.y, 0.f), F::mn(y.z, 0.f), F::mn(y.w, 0.f))
+                         : make_float4(F::mx(y.x, 0.f), F::mx(y.y, 0.f), F::mx(y.z, 0.f), F::mx(y.w, 0.f));
       }
   }
 
-  __device__ __forceinline__ float2 score(const SelectArgs& a, const int64_t (&tile)[2]) {
+  __device__ __forceinline__ void load(const SelectArgs& a, const int64_t (&tile)[2]) {
+    bounds = static_cast<const float*>(a.bounds);
+    now[0] = tile[0];
+    now[1] = tile[1];
+  }
+
+  __device__ __forceinline__ float2 score(float* largest) {
     using F = MinMax<float>;
-    const int lane = threadIdx.x & 31, gq = lane >> 2;
+    const int lane = threadIdx.x & 31;
     float2 out = make_float2(0.f, 0.f);
+    float big = 0.f;
 #pragma unroll 1
     for (int r0 = 0; r0 < 16; r0 += 4) {
-      float4 x[4][kPieces];
+      float4 y[4][kPieces];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        // row r0 + r lies with lane 4 (row mod 8), in tile[row / 8]
-        const int64_t t = __shfl_sync(kFull, r0 < 8 ? tile[0] : tile[1], 4 * ((r0 + r) & 7));
-        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.bounds) + t * 2 * D) + lane;
+        // row r0 + r lies with lane 4 (row mod 8), in now[row / 8]
+        const int64_t t = __shfl_sync(kFull, r0 < 8 ? now[0] : now[1], 4 * ((r0 + r) & 7));
+        const float4* src = reinterpret_cast<const float4*>(bounds + t * 2 * D) + lane;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) x[r][i] = __ldg(src + 32 * i);
+        for (int i = 0; i < kPieces; ++i) y[r][i] = __ldg(src + 32 * i);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float best = 0.f;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-          big = F::mx(big, F::mx(F::mx(fabsf(x[r][i].x), fabsf(x[r][i].y)), F::mx(fabsf(x[r][i].z), fabsf(x[r][i].w))));
+          big = F::mx(big, F::mx(F::mx(fabsf(y[r][i].x), fabsf(y[r][i].y)), F::mx(fabsf(y[r][i].z), fabsf(y[r][i].w))));
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           float s = 0.f;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i)
-            s += q[h][i].x * x[r][i].x + q[h][i].y * x[r][i].y + q[h][i].z * x[r][i].z + q[h][i].w * x[r][i].w;
+            s += q[h][i].x * y[r][i].x + q[h][i].y * y[r][i].y + q[h][i].z * y[r][i].z + q[h][i].w * y[r][i].w;
 #pragma unroll
           for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
           best = h ? F::mx(best, s) : s;
         }
-        if (gq == ((r0 + r) & 7)) {
+        if ((lane >> 2) == ((r0 + r) & 7)) {
           if (r0 < 8) out.x = best;
           else out.y = best;
         }
       }
     }
+    *largest = big;
     return out;
   }
-
-  __device__ __forceinline__ float largest() const { return big; }
 };
+
+// Bytes bound it: 2 D elements per block and KV head, read once for the G
+// heads of the group.  The tiles of 16 blocks of all rows that have a choice
+// to make are numbered in order and dealt out to the warps of a resident grid
+// in equal runs, whatever the mix of lengths: a warp keeps q of its row in
+// registers and streams the row's tiles.
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreSeqs = 1024;  // sequences numbered at a time
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectArgs a) {
+  __shared__ int first[kScoreSeqs + 1];  // tiles of a KV head before each sequence
+  __shared__ int sums[kScoreWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2;
+  // neighbouring runs go to different SMs, so that a short list uses them all
+  const int64_t w = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, nw = static_cast<int64_t>(gridDim.x) * kScoreWarps;
+
+  for (int b0 = 0; b0 < a.num_seqs; b0 += kScoreSeqs) {
+    const int nb = min(kScoreSeqs, a.num_seqs - b0);
+    constexpr int kPer = kScoreSeqs / kScoreThreads;
+    int count[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int k = tid * kPer + i;
+      const int nblk = k < nb ? blocks_of(a, b0 + k, false) : 0;
+      count[i] = nblk > a.max_selected ? (nblk + 15) / 16 : 0;
+      mine += count[i];
+    }
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, before, o);
+      if (lane >= o) before += y;
+    }
+    __syncthreads();  // the numbers of the sequences before are no longer read
+    if (lane == 31) sums[warp] = before;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kScoreWarps; ++x)
+      if (x < warp) before += sums[x];
+    before -= mine;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      first[tid * kPer + i] = before;
+      before += count[i];
+    }
+    if (tid == kScoreThreads - 1) first[kScoreSeqs] = before;
+    __syncthreads();
+    const int64_t total = static_cast<int64_t>(first[kScoreSeqs]) * a.num_kv_heads;
+    int64_t p = total * w / nw;
+    const int64_t end = total * (w + 1) / nw;
+    if (p >= end) continue;
+
+    int lo = 0, hi = nb - 1;  // the last sequence whose first tile is at or before p (a row without tiles is not)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(first[mid]) * a.num_kv_heads <= p) lo = mid;
+      else hi = mid - 1;
+    }
+    int b = lo, tiles = first[b + 1] - first[b];
+    int g = static_cast<int>((p - static_cast<int64_t>(first[b]) * a.num_kv_heads) / tiles);
+    int t = static_cast<int>(p - static_cast<int64_t>(first[b]) * a.num_kv_heads - static_cast<int64_t>(g) * tiles);
+    int nblk = blocks_of(a, b0 + b, false);
+    auto entry = [&](int r) {  // of row gq + 8 r of the tile at hand
+      return a.block_tables[static_cast<int64_t>(b0 + b) * a.max_blocks + min(t * 16 + gq + 8 * r, nblk - 1)];
+    };
+    int32_t phys[2] = {entry(0), entry(1)};
+    Scorer<T, D, G> scorer;
+    scorer.group(a, b0 + b, g);
+    for (;;) {
+      const int64_t tile[2] = {bounds_tile(a, phys[0], g), bounds_tile(a, phys[1], g)};
+      scorer.load(a, tile);
+      const int64_t row = static_cast<int64_t>(b0 + b) * a.num_kv_heads + g;
+      const int j0 = t * 16 + gq, c1 = nblk - a.n_last, blocks = nblk, at = t;
+      // the tile after, and its table entries
+      const bool more = ++p < end;
+      bool other = false;
+      if (more) {
+        if (++t == tiles) {
+          t = 0;
+          other = true;
+          if (++g == a.num_kv_heads) {
+            g = 0;
+            do ++b;
+            while (first[b + 1] == first[b]);
+            tiles = first[b + 1] - first[b];
+            nblk = blocks_of(a, b0 + b, false);
+          }
+        }
+        phys[0] = entry(0);
+        phys[1] = entry(1);
+      }
+      float big;
+      const float2 s = scorer.score(&big);
+      uint32_t mn = 0xffffffffu, mx = 0;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int j = j0 + 8 * r;
+        const float x = r ? s.y : s.x;
+        if ((lane & 3) == 0 && j < blocks) a.scores[row * a.max_blocks + j] = x;
+        if (j >= a.n_first && j < c1) {
+          const uint32_t key = key32(x);
+          mn = min(mn, key);
+          mx = max(mx, key);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
+      mn = __reduce_min_sync(kFull, mn);
+      mx = __reduce_max_sync(kFull, mx);
+      if (lane == 0) a.stats[row * a.tiles + at] = TileStats{mn, mx, big, 0.f};
+      if (!more) break;
+      if (other) scorer.group(a, b0 + b, g);
+    }
+  }
+}
 
 // The score of block j in 64 bits (all lanes of the warp get its key).
 template <typename T, int D, int G>
@@ -456,7 +578,7 @@ __device__ __forceinline__ uint64_t fine_key(const SelectArgs& a, int b, int g, 
   using Q = typename QueryOf<T>::type;
   constexpr int kPer = D / 32;  // a lane's channels, adjacent
   const int d0 = (threadIdx.x & 31) * kPer;
-  const int64_t at = bounds_tile(a, b, j, g) * 2 * D + d0;
+  const int64_t at = bounds_tile(a, a.block_tables[static_cast<int64_t>(b) * a.max_blocks + j], g) * 2 * D + d0;
   double lo[kPer], hi[kPer], s[G];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -526,87 +648,23 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
   __shared__ uint64_t fine[kSelectFine];
   __shared__ int fine_at[kSelectFine];
   __shared__ int red[kSelectWarps], two[2], count[2];
-  __shared__ SelectStats warp_stats[kSelectWarps];
+  __shared__ TileStats warp_stats[kSelectWarps];
   __shared__ float q_norm[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  uint32_t rank, ctas;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-  const int64_t row = blockIdx.x / ctas;
+  const int64_t row = blockIdx.x;
   const int b = static_cast<int>(row / a.num_kv_heads), g = static_cast<int>(row - static_cast<int64_t>(b) * a.num_kv_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nblk = blocks_of(a, b, rank == 0 && g == 0 && tid == 0);
+  const int nblk = blocks_of(a, b, g == 0 && tid == 0);
   const int K = a.max_selected;
   int32_t* out = a.selected + row * K;
   if (nblk <= K) {  // every block
-    if (rank == 0)
-      for (int i = tid; i < K; i += kSelectThreads) out[i] = i < nblk ? i : -1;
+    for (int i = tid; i < K; i += kSelectThreads) out[i] = i < nblk ? i : -1;
     return;
   }
   const int c0 = a.n_first, c1 = nblk - a.n_last;  // the candidates: more than are needed, since nblk > K
   const int need0 = K - a.n_first - a.n_last;
-  float* row_scores = a.scores + row * a.max_blocks;
-  SelectStats* row_stats = a.stats + row * kSelectCluster;
-
-  if (need0 > 0) {
-    // ---- 32-bit scores of this CTA's slice ----
-    const int tiles = (nblk + 15) / 16;
-    const int per = (tiles + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
-    const int t1 = min(tiles, (static_cast<int>(rank) + 1) * per);
-    Scorer<T, D, G> scorer;
-    scorer.init(a, b, g);
-    uint32_t mn = 0xffffffffu, mx = 0;
-    for (int t = static_cast<int>(rank) * per + warp; t < t1; t += kSelectWarps) {
-      const int gq = lane >> 2;
-      int64_t tile[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) tile[r] = bounds_tile(a, b, min(t * 16 + gq + 8 * r, nblk - 1), g);
-      const float2 s = scorer.score(a, tile);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int j = t * 16 + gq + 8 * r;
-        const float x = r ? s.y : s.x;
-        if ((lane & 3) == 0 && j < nblk) row_scores[j] = x;
-        if (j >= c0 && j < c1) {
-          const uint32_t k = key32(x);
-          mn = min(mn, k);
-          mx = max(mx, k);
-        }
-      }
-    }
-    float big = scorer.largest();
-#pragma unroll
-    for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
-    mn = __reduce_min_sync(kFull, mn);
-    mx = __reduce_max_sync(kFull, mx);
-    if (lane == 0) warp_stats[warp] = SelectStats{mn, mx, big, 0.f};
-    if (rank == 0 && warp < G) {  // sum |q| of each head, for the error bound
-      float s = 0.f;
-      for (int d = lane; d < D; d += 32)
-        s += fabsf(widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + warp) * D + d]));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-      if (lane == 0) q_norm[warp] = s;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      SelectStats st = warp_stats[0];
-      for (int w = 1; w < kSelectWarps; ++w) {
-        st.min_key = min(st.min_key, warp_stats[w].min_key);
-        st.max_key = max(st.max_key, warp_stats[w].max_key);
-        st.big = MinMax<float>::mx(st.big, warp_stats[w].big);
-      }
-      row_stats[rank] = st;
-    }
-    // every CTA's scores and statistics are in the workspace
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (rank != 0) return;
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  } else if (rank != 0) {
-    return;
-  }
-
+  const float* row_scores = a.scores + row * a.max_blocks;
   const int words = (nblk + 31) / 32;
   for (int i = tid; i < words; i += kSelectThreads) {  // the first and the last blocks
     uint32_t m = 0;
@@ -623,13 +681,40 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
       for (int j = tid; j < nblk; j += kSelectThreads) copy[j] = row_scores[j];
       scores = copy;
     }
+    if (warp < G) {  // sum |q| of each head, for the error bound
+      float s = 0.f;
+#pragma unroll
+      for (int d = 0; d < D; d += 32)
+        s += fabsf(widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + warp) * D + d + lane]));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+      if (lane == 0) q_norm[warp] = s;
+    }
+    {
+      uint32_t mn = 0xffffffffu, mx = 0;
+      float big = 0.f;
+      for (int t = tid; t < (nblk + 15) / 16; t += kSelectThreads) {
+        const TileStats st = a.stats[row * a.tiles + t];
+        mn = min(mn, st.min_key);
+        mx = max(mx, st.max_key);
+        big = MinMax<float>::mx(big, st.big);
+      }
+      mn = __reduce_min_sync(kFull, mn);
+      mx = __reduce_max_sync(kFull, mx);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
+      if (lane == 0) warp_stats[warp] = TileStats{mn, mx, big, 0.f};
+    }
+    for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
+    if (tid < 2) count[tid] = 0;
+    __syncthreads();
     uint32_t base = 0xffffffffu, last = 0;
     float big = 0.f, q1 = 0.f;
-    for (uint32_t r = 0; r < ctas; ++r) {
-      const SelectStats st = row_stats[r];
-      base = min(base, st.min_key);
-      last = max(last, st.max_key);
-      big = MinMax<float>::mx(big, st.big);
+#pragma unroll
+    for (int w = 0; w < kSelectWarps; ++w) {
+      base = min(base, warp_stats[w].min_key);
+      last = max(last, warp_stats[w].max_key);
+      big = MinMax<float>::mx(big, warp_stats[w].big);
     }
 #pragma unroll
     for (int h = 0; h < G; ++h) q1 = MinMax<float>::mx(q1, q_norm[h]);
@@ -643,8 +728,6 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
       for (;;) {  // each round keeps less than 1 / 512 of the range
         int shift = 0;
         while (((last - base) >> shift) >= kSelectBins) ++shift;
-        for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
         for (int j = c0 + tid; j < c1; j += kSelectThreads) {
           const uint32_t k = key32(scores[j]);
           if (k >= base && k <= last) atomicAdd(&hist[(k - base) >> shift], 1);
@@ -657,8 +740,10 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
         base += static_cast<uint32_t>(bin) << shift;
         const uint32_t width = (1u << shift) - 1;
         if (last - base > width) last = base + width;
-        __syncthreads();
         if (shift == 0 || in_bin <= 8) break;
+        __syncthreads();
+        for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
+        __syncthreads();
       }
       t_lo = unkey32(base);
       t_hi = unkey32(last);
@@ -670,8 +755,6 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
     // t_hi + eps, and likewise at least t_lo - eps.
     const float in_above = bounded ? t_hi + 2.f * eps : INFINITY;
     const float out_below = bounded ? t_lo - 2.f * eps : -INFINITY;
-    if (tid < 2) count[tid] = 0;
-    __syncthreads();
     for (int j0 = 0; j0 < words * 32; j0 += kSelectThreads) {
       const int j = j0 + tid;
       bool in = false, near = false;
@@ -724,7 +807,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
       uint64_t prefix = 0;
       int left = need;
       for (int shift = 56; shift >= 0; shift -= 8) {
-        hist[tid] = 0;  // 256 bins
+        hist[tid] = 0;  // kSelectThreads bins, 256 of them in use
         __syncthreads();
         for (int j = c0 + tid; j < c1; j += kSelectThreads) {
           const float s = scores[j];
@@ -734,7 +817,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
         }
         __syncthreads();
         int above;
-        const int bin = find_bin(hist, 256, left, &above, red, two);
+        const int bin = find_bin(hist, kSelectThreads, left, &above, red, two);
         left -= above;
         prefix |= static_cast<uint64_t>(bin) << shift;
         __syncthreads();

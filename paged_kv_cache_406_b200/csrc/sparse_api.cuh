@@ -45,51 +45,37 @@ struct SelectLayout {
 SelectLayout select_layout(int64_t rows, int64_t max_blocks) {
   SelectLayout w;
   w.stats = round256(static_cast<size_t>(rows * max_blocks) * sizeof(float));
-  w.fine = w.stats + round256(static_cast<size_t>(rows) * pkv::kSelectCluster * sizeof(pkv::SelectStats));
+  w.fine = w.stats + round256(static_cast<size_t>(rows * ((max_blocks + 15) / 16)) * sizeof(pkv::TileStats));
   w.total = w.fine + round256(static_cast<size_t>(rows * max_blocks) * sizeof(uint64_t));
   return w;
 }
 
-// Shared memory of a selecting CTA: the bitmap, and a copy of the scores where
-// it leaves room for two CTAs on an SM.
+// Scores that a selecting CTA copies to shared memory: what leaves room for
+// two CTAs on an SM.
 constexpr int32_t kSelectSmemScores = 16384;
 
 template <typename T, int D, int G>
 int launch_select(pkv::SelectArgs a, const char* fn, cudaStream_t s) {
-  auto kern = pkv::select_kernel<T, D, G>;
   const int64_t rows = int64_t(a.num_seqs) * a.num_kv_heads;
-  // CTAs of a row: as many as keep the row's tiles of 16 blocks two to a warp
-  // and the grid within three rounds of two CTAs an SM
-  int ctas = 1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  const int64_t tiles = (int64_t(a.max_blocks) + 15) / 16;
-  while (ctas < pkv::kSelectCluster && rows * ctas * 2 <= 6 * int64_t(sm_count(dev)) &&
-         tiles > int64_t(2) * ctas * pkv::kSelectWarps)
-    ctas *= 2;
-  a.smem_scores = a.max_blocks <= kSelectSmemScores ? a.max_blocks : 0;
-  const size_t smem = static_cast<size_t>((a.max_blocks + 31) / 32 + a.smem_scores) * 4;
+  auto kern = pkv::select_kernel<T, D, G>;
   static std::atomic<bool> opted[kMaxDevices];
   if (dev >= kMaxDevices || !opted[dev].load(std::memory_order_relaxed)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSelectBlocks / 8));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select)");
     if (dev < kMaxDevices) opted[dev].store(true, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
-  cfg.blockDim = dim3(pkv::kSelectThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (a.max_blocks > a.max_selected && a.max_selected > a.n_first + a.n_last) {  // else no score decides
+    const int64_t ctas = (rows * a.tiles + pkv::kScoreWarps - 1) / pkv::kScoreWarps;  // a tile a warp
+    e = launch_pdl(pkv::score_kernel<T, D, G>, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, 2 * sm_count(dev)))),
+                   dim3(pkv::kScoreThreads), 0, s, a);
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+  }
+  a.smem_scores = a.max_blocks <= kSelectSmemScores ? a.max_blocks : 0;
+  const size_t smem = static_cast<size_t>((a.max_blocks + 31) / 32 + a.smem_scores) * 4;
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(pkv::kSelectThreads), smem, s, a);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return pkv::ok();
 }
@@ -243,6 +229,8 @@ extern "C" int pkv_block_select(const void* q, const void* bounds, const int32_t
   const SelectLayout w = select_layout(rows, max_blocks_per_seq);
   if (workspace_bytes < w.total)
     return fail(PKV_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, w.total);
+  if (rows * ((max_blocks_per_seq + 15) / 16) > INT32_MAX)
+    return fail(PKV_ERR_INVALID_ARG, "%s: too many blocks in one call", fn);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   pkv::SelectArgs a{};
   a.q = q;
@@ -250,7 +238,7 @@ extern "C" int pkv_block_select(const void* q, const void* bounds, const int32_t
   a.block_tables = block_tables;
   a.seq_lens = seq_lens;
   a.scores = reinterpret_cast<float*>(ws);
-  a.stats = reinterpret_cast<pkv::SelectStats*>(ws + w.stats);
+  a.stats = reinterpret_cast<pkv::TileStats*>(ws + w.stats);
   a.fine = reinterpret_cast<uint64_t*>(ws + w.fine);
   a.selected = selected;
   a.num_seqs = num_seqs;
@@ -262,6 +250,7 @@ extern "C" int pkv_block_select(const void* q, const void* bounds, const int32_t
   a.max_selected = max_selected;
   a.n_first = n_first;
   a.n_last = n_last;
+  a.tiles = (max_blocks_per_seq + 15) / 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool d128 = head_dim == 128;
   switch (dtype) {
