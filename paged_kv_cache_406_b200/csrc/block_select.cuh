@@ -221,8 +221,6 @@ struct SelectArgs {
   int32_t smem_scores;  // blocks whose scores fit the shared memory of the launch (0: re-read them)
 };
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectBins = 1024;
 constexpr int kSelectFine = 512;    // border blocks ranked in shared memory
 
@@ -258,15 +256,11 @@ struct QueryOf { using type = T; };
 template <>
 struct QueryOf<E4m3> { using type = __half; };
 
-// Element i of a bounds array as a float.
+// A bound as a float.
 template <typename T>
-__device__ __forceinline__ float bound_at(const void* base, int64_t i) {
-  if constexpr (std::is_same_v<T, E4m3>) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(base)[i], __NV_E4M3);
-    return __half2float(__half(h));
-  } else {
-    return widen1<T>(static_cast<const T*>(base)[i]);
-  }
+__device__ __forceinline__ float bound_value(T x) {
+  if constexpr (std::is_same_v<T, E4m3>) return __half2float(__half(__nv_cvt_fp8_to_halfraw(x.code, __NV_E4M3)));
+  else return widen1<T>(x);
 }
 
 // Order-preserving map of floats to unsigned integers; NaN above everything.
@@ -460,28 +454,38 @@ struct Scorer<float, D, G> {
 // registers and streams the row's tiles.
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreSeqs = 1024;  // sequences numbered at a time
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectArgs a) {
-  __shared__ int first[kScoreSeqs + 1];  // tiles of a KV head before each sequence
-  __shared__ int sums[kScoreWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2;
+  // Every warp numbers the tiles by itself, 128 sequences (four a lane) at a
+  // time; a short batch then waits for one trip to memory and no barrier.
+  constexpr int kPer = 4;
+  auto tiles_of = [&](int b) {
+    const int nblk = b < a.num_seqs ? blocks_of(a, b, false) : 0;
+    return nblk > a.max_selected ? (nblk + 15) / 16 : 0;
+  };
+  int count[kPer], mine = 0, total = 0;
+  for (int b0 = (a.num_seqs - 1) / (32 * kPer) * (32 * kPer); b0 >= 0; b0 -= 32 * kPer) {  // ends with the first 128
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) mine += count[i] = tiles_of(b0 + lane * kPer + i);
+    total += __reduce_add_sync(kFull, mine);
+  }
   // neighbouring runs go to different SMs, so that a short list uses them all
   const int64_t w = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, nw = static_cast<int64_t>(gridDim.x) * kScoreWarps;
-
-  for (int b0 = 0; b0 < a.num_seqs; b0 += kScoreSeqs) {
-    const int nb = min(kScoreSeqs, a.num_seqs - b0);
-    constexpr int kPer = kScoreSeqs / kScoreThreads;
-    int count[kPer], mine = 0;
+  const int64_t all = static_cast<int64_t>(total) * a.num_kv_heads;
+  int64_t p = all * w / nw;
+  const int64_t end = all * (w + 1) / nw;
+  if (p >= end) return;
+  int b = 0, first = 0;  // the sequence of tile p, and the tiles of a KV head before it
+  for (int b0 = 0, done = 0;; b0 += 32 * kPer) {
+    if (b0) {
+      mine = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int k = tid * kPer + i;
-      const int nblk = k < nb ? blocks_of(a, b0 + k, false) : 0;
-      count[i] = nblk > a.max_selected ? (nblk + 15) / 16 : 0;
-      mine += count[i];
+      for (int i = 0; i < kPer; ++i) mine += count[i] = tiles_of(b0 + lane * kPer + i);
     }
     int before = mine;
 #pragma unroll
@@ -489,134 +493,138 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectArg
       const int y = __shfl_up_sync(kFull, before, o);
       if (lane >= o) before += y;
     }
-    __syncthreads();  // the numbers of the sequences before are no longer read
-    if (lane == 31) sums[warp] = before;
-    __syncthreads();
+    const int sum = __shfl_sync(kFull, before, 31);
+    before += done - mine;
+    const bool here = static_cast<int64_t>(before) * a.num_kv_heads <= p && static_cast<int64_t>(before + mine) * a.num_kv_heads > p;
+    const uint32_t m = __ballot_sync(kFull, here);
+    if (m) {
+      int at = b0 + lane * kPer;
 #pragma unroll
-    for (int x = 0; x < kScoreWarps; ++x)
-      if (x < warp) before += sums[x];
-    before -= mine;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      first[tid * kPer + i] = before;
-      before += count[i];
-    }
-    if (tid == kScoreThreads - 1) first[kScoreSeqs] = before;
-    __syncthreads();
-    const int64_t total = static_cast<int64_t>(first[kScoreSeqs]) * a.num_kv_heads;
-    int64_t p = total * w / nw;
-    const int64_t end = total * (w + 1) / nw;
-    if (p >= end) continue;
-
-    int lo = 0, hi = nb - 1;  // the last sequence whose first tile is at or before p (a row without tiles is not)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(first[mid]) * a.num_kv_heads <= p) lo = mid;
-      else hi = mid - 1;
-    }
-    int b = lo, tiles = first[b + 1] - first[b];
-    int g = static_cast<int>((p - static_cast<int64_t>(first[b]) * a.num_kv_heads) / tiles);
-    int t = static_cast<int>(p - static_cast<int64_t>(first[b]) * a.num_kv_heads - static_cast<int64_t>(g) * tiles);
-    int nblk = blocks_of(a, b0 + b, false);
-    auto entry = [&](int r) {  // of row gq + 8 r of the tile at hand
-      return a.block_tables[static_cast<int64_t>(b0 + b) * a.max_blocks + min(t * 16 + gq + 8 * r, nblk - 1)];
-    };
-    int32_t phys[2] = {entry(0), entry(1)};
-    Scorer<T, D, G> scorer;
-    scorer.group(a, b0 + b, g);
-    for (;;) {
-      const int64_t tile[2] = {bounds_tile(a, phys[0], g), bounds_tile(a, phys[1], g)};
-      scorer.load(a, tile);
-      const int64_t row = static_cast<int64_t>(b0 + b) * a.num_kv_heads + g;
-      const int j0 = t * 16 + gq, c1 = nblk - a.n_last, blocks = nblk, at = t;
-      // the tile after, and its table entries
-      const bool more = ++p < end;
-      bool other = false;
-      if (more) {
-        if (++t == tiles) {
-          t = 0;
-          other = true;
-          if (++g == a.num_kv_heads) {
-            g = 0;
-            do ++b;
-            while (first[b + 1] == first[b]);
-            tiles = first[b + 1] - first[b];
-            nblk = blocks_of(a, b0 + b, false);
-          }
+      for (int i = 0; i < kPer - 1; ++i)
+        if (at == b0 + lane * kPer + i && static_cast<int64_t>(before + count[i]) * a.num_kv_heads <= p) {
+          before += count[i];
+          ++at;
         }
-        phys[0] = entry(0);
-        phys[1] = entry(1);
-      }
-      float big;
-      const float2 s = scorer.score(&big);
-      uint32_t mn = 0xffffffffu, mx = 0;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int j = j0 + 8 * r;
-        const float x = r ? s.y : s.x;
-        if ((lane & 3) == 0 && j < blocks) a.scores[row * a.max_blocks + j] = x;
-        if (j >= a.n_first && j < c1) {
-          const uint32_t key = key32(x);
-          mn = min(mn, key);
-          mx = max(mx, key);
+      b = __shfl_sync(kFull, at, __ffs(m) - 1);
+      first = __shfl_sync(kFull, before, __ffs(m) - 1);
+      break;
+    }
+    done += sum;
+  }
+  int nblk = blocks_of(a, b, false), tiles = (nblk + 15) / 16;
+  const int64_t off = p - static_cast<int64_t>(first) * a.num_kv_heads;
+  int g = static_cast<int>(off / tiles), t = static_cast<int>(off - static_cast<int64_t>(g) * tiles);
+  auto entry = [&](int r) {  // of row gq + 8 r of the tile at hand
+    return a.block_tables[static_cast<int64_t>(b) * a.max_blocks + min(t * 16 + gq + 8 * r, nblk - 1)];
+  };
+  int32_t phys[2] = {entry(0), entry(1)};
+  Scorer<T, D, G> scorer;
+  scorer.group(a, b, g);
+  for (;;) {
+    const int64_t tile[2] = {bounds_tile(a, phys[0], g), bounds_tile(a, phys[1], g)};
+    scorer.load(a, tile);
+    const int64_t row = static_cast<int64_t>(b) * a.num_kv_heads + g;
+    const int j0 = t * 16 + gq, c1 = nblk - a.n_last, blocks = nblk, at = t;
+    // the tile after, and its table entries
+    const bool more = ++p < end;
+    bool other = false;
+    if (more) {
+      if (++t == tiles) {
+        t = 0;
+        other = true;
+        if (++g == a.num_kv_heads) {
+          g = 0;
+          do tiles = tiles_of(++b);  // there is one: p < end
+          while (tiles == 0);
+          nblk = blocks_of(a, b, false);
         }
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
-      mn = __reduce_min_sync(kFull, mn);
-      mx = __reduce_max_sync(kFull, mx);
-      if (lane == 0) a.stats[row * a.tiles + at] = TileStats{mn, mx, big, 0.f};
-      if (!more) break;
-      if (other) scorer.group(a, b0 + b, g);
+      phys[0] = entry(0);
+      phys[1] = entry(1);
     }
+    float big;
+    const float2 s = scorer.score(&big);
+    uint32_t mn = 0xffffffffu, mx = 0;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int j = j0 + 8 * r;
+      const float x = r ? s.y : s.x;
+      if ((lane & 3) == 0 && j < blocks) a.scores[row * a.max_blocks + j] = x;
+      if (j >= a.n_first && j < c1) {
+        const uint32_t key = key32(x);
+        mn = min(mn, key);
+        mx = max(mx, key);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
+    mn = __reduce_min_sync(kFull, mn);
+    mx = __reduce_max_sync(kFull, mx);
+    if (lane == 0) a.stats[row * a.tiles + at] = TileStats{mn, mx, big, 0.f};
+    if (!more) break;
+    if (other) scorer.group(a, b, g);
   }
 }
 
-// The score of block j in 64 bits (all lanes of the warp get its key).
+// The score of block j in 64 bits, as a key (in all lanes of the warp).  q:
+// the group's rows in 64 bits, in shared memory.
 template <typename T, int D, int G>
-__device__ __forceinline__ uint64_t fine_key(const SelectArgs& a, int b, int g, int j) {
-  using Q = typename QueryOf<T>::type;
+__device__ __forceinline__ uint64_t fine_key(const SelectArgs& a, const double (&q)[G][D], int b, int g, int j) {
   constexpr int kPer = D / 32;  // a lane's channels, adjacent
-  const int d0 = (threadIdx.x & 31) * kPer;
-  const int64_t at = bounds_tile(a, a.block_tables[static_cast<int64_t>(b) * a.max_blocks + j], g) * 2 * D + d0;
-  double lo[kPer], hi[kPer], s[G];
+  const int lane = threadIdx.x & 31, d0 = lane * kPer;
+  const int64_t tile = bounds_tile(a, a.block_tables[static_cast<int64_t>(b) * a.max_blocks + j], g);
+  const T* src = static_cast<const T*>(a.bounds) + tile * 2 * D + d0;
+  using C = Chunk<T, kPer>;
+  C lows, highs;
+  lows.raw = *reinterpret_cast<const typename C::Raw*>(src);
+  highs.raw = *reinterpret_cast<const typename C::Raw*>(src + D);
+  double s[G];
+#pragma unroll
+  for (int h = 0; h < G; ++h) s[h] = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    lo[i] = bound_at<T>(a.bounds, at + i);
-    hi[i] = bound_at<T>(a.bounds, at + D + i);
-  }
+    const double lo = bound_value(lows.e[i]), hi = bound_value(highs.e[i]);
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
-    s[h] = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float x = widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + h) * D + d0 + i]);
-      const double xn = x > 0.f ? 0.0 : x, xp = x < 0.f ? 0.0 : x;
-      s[h] += xn * lo[i] + xp * hi[i];
+    for (int h = 0; h < G; ++h) {
+      const double x = q[h][d0 + i];
+      s[h] += (x > 0 ? 0.0 : x) * lo + (x < 0 ? 0.0 : x) * hi;
     }
   }
+  // sums over the lanes: while there are heads to share out, a lane keeps
+  // half of them and passes the other half on
+  int n = G;
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
+  for (int o = 16; o; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & o;
 #pragma unroll
-    for (int h = 0; h < G; ++h) s[h] += __shfl_xor_sync(kFull, s[h], o);
-  uint64_t best = 0;
+      for (int h = 0; h < G / 2; ++h)
+        if (h < n) s[h] = (up ? s[h + n] : s[h]) + __shfl_xor_sync(kFull, up ? s[h] : s[h + n], o);
+    } else {
+      s[0] += __shfl_xor_sync(kFull, s[0], o);
+    }
+  }
+  uint64_t best = key64(s[0]);
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
-    const uint64_t k = key64(s[h]);
-    best = k > best ? k : best;
+  for (int o = 16; o > 16 / G; o >>= 1) {
+    const uint64_t y = __shfl_xor_sync(kFull, best, o);
+    best = y > best ? y : best;
   }
   return best;
 }
 
-// Finds in hist[0 .. bins) (counts per bin, larger keys in higher bins; bins a
-// multiple of the threads) the bin in which the need-th largest lies; *above:
-// the count in higher bins.  One count must reach `need`.
-__device__ __forceinline__ int find_bin(const int* hist, int bins, int need, int* above, int* red, int* two) {
-  const int per = bins / kSelectThreads;
-  const int top = bins - 1 - static_cast<int>(threadIdx.x) * per;  // this thread's highest bin
+// Finds in hist[0 .. kBins) (counts per bin, larger keys in higher bins) the
+// bin in which the need-th largest lies; *above: the count in higher bins.
+// One count must reach `need`.
+template <int kThreads, int kBins>
+__device__ __forceinline__ int find_bin(const int* hist, int need, int* above, int* red, int* two) {
+  constexpr int kPer = kBins / kThreads;
+  const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kPer;  // this thread's highest bin
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) mine += hist[top - i];
+  int h[kPer], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) mine += h[i] = hist[top - i];
   int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -626,13 +634,18 @@ __device__ __forceinline__ int find_bin(const int* hist, int bins, int need, int
   if (lane == 31) red[warp] = before;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w)
+  for (int w = 0; w < kThreads / 32; ++w)
     if (w < warp) before += red[w];
   before -= mine;
   if (before < need && before + mine >= need) {
-    int run = before, i = 0;
-    while (i < per - 1 && run + hist[top - i] < need) run += hist[top - i++];
-    two[0] = top - i;
+    int run = before, bin = top;
+#pragma unroll
+    for (int i = 0; i < kPer - 1; ++i)
+      if (bin == top - i && run + h[i] < need) {
+        run += h[i];
+        --bin;
+      }
+    two[0] = bin;
     two[1] = run;
   }
   __syncthreads();
@@ -640,33 +653,48 @@ __device__ __forceinline__ int find_bin(const int* hist, int bins, int need, int
   return two[0];
 }
 
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectArgs a) {
+template <typename T, int D, int G, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_kernel(const SelectArgs a) {
   using Q = typename QueryOf<T>::type;
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ uint32_t bitmap[];  // one bit per block, then the scores of up to smem_scores blocks
   __shared__ int hist[kSelectBins];
   __shared__ uint64_t fine[kSelectFine];
   __shared__ int fine_at[kSelectFine];
-  __shared__ int red[kSelectWarps], two[2], count[2];
-  __shared__ TileStats warp_stats[kSelectWarps];
-  __shared__ float q_norm[8];
+  __shared__ int red[kWarps], two[2], count[2];
+  __shared__ TileStats warp_stats[kWarps];
+  __shared__ double q_fine[G][D];
+  __shared__ float q_norm[G];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t row = blockIdx.x;
   const int b = static_cast<int>(row / a.num_kv_heads), g = static_cast<int>(row - static_cast<int64_t>(b) * a.num_kv_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp < G) {  // q in 64 bits, and sum |q| of each head for the error bound
+    float s = 0.f;
+#pragma unroll
+    for (int d = 0; d < D; d += 32) {
+      const float x =
+          widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + warp) * D + d + lane]);
+      q_fine[warp][d + lane] = x;
+      s += fabsf(x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    if (lane == 0) q_norm[warp] = s;
+  }
   const int nblk = blocks_of(a, b, g == 0 && tid == 0);
   const int K = a.max_selected;
   int32_t* out = a.selected + row * K;
   if (nblk <= K) {  // every block
-    for (int i = tid; i < K; i += kSelectThreads) out[i] = i < nblk ? i : -1;
+    for (int i = tid; i < K; i += kThreads) out[i] = i < nblk ? i : -1;
     return;
   }
   const int c0 = a.n_first, c1 = nblk - a.n_last;  // the candidates: more than are needed, since nblk > K
   const int need0 = K - a.n_first - a.n_last;
   const float* row_scores = a.scores + row * a.max_blocks;
   const int words = (nblk + 31) / 32;
-  for (int i = tid; i < words; i += kSelectThreads) {  // the first and the last blocks
+  for (int i = tid; i < words; i += kThreads) {  // the first and the last blocks
     uint32_t m = 0;
     if (i * 32 < c0) m |= c0 - i * 32 >= 32 ? kFull : (1u << (c0 - i * 32)) - 1;
     if (i * 32 + 32 > c1) m |= c1 <= i * 32 ? kFull : kFull << (c1 - i * 32);
@@ -678,22 +706,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
     const float* scores = row_scores;
     if (nblk <= a.smem_scores) {
       float* copy = reinterpret_cast<float*>(bitmap + (a.max_blocks + 31) / 32);
-      for (int j = tid; j < nblk; j += kSelectThreads) copy[j] = row_scores[j];
+      for (int j = tid; j < nblk; j += kThreads) copy[j] = row_scores[j];
       scores = copy;
-    }
-    if (warp < G) {  // sum |q| of each head, for the error bound
-      float s = 0.f;
-#pragma unroll
-      for (int d = 0; d < D; d += 32)
-        s += fabsf(widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + warp) * D + d + lane]));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-      if (lane == 0) q_norm[warp] = s;
     }
     {
       uint32_t mn = 0xffffffffu, mx = 0;
       float big = 0.f;
-      for (int t = tid; t < (nblk + 15) / 16; t += kSelectThreads) {
+      for (int t = tid; t < (nblk + 15) / 16; t += kThreads) {
         const TileStats st = a.stats[row * a.tiles + t];
         mn = min(mn, st.min_key);
         mx = max(mx, st.max_key);
@@ -705,13 +724,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
       for (int o = 16; o; o >>= 1) big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
       if (lane == 0) warp_stats[warp] = TileStats{mn, mx, big, 0.f};
     }
-    for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
+    for (int i = tid; i < kSelectBins; i += kThreads) hist[i] = 0;
     if (tid < 2) count[tid] = 0;
     __syncthreads();
     uint32_t base = 0xffffffffu, last = 0;
     float big = 0.f, q1 = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       base = min(base, warp_stats[w].min_key);
       last = max(last, warp_stats[w].max_key);
       big = MinMax<float>::mx(big, warp_stats[w].big);
@@ -728,13 +747,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
       for (;;) {  // each round keeps less than 1 / 512 of the range
         int shift = 0;
         while (((last - base) >> shift) >= kSelectBins) ++shift;
-        for (int j = c0 + tid; j < c1; j += kSelectThreads) {
+        for (int j = c0 + tid; j < c1; j += kThreads) {
           const uint32_t k = key32(scores[j]);
           if (k >= base && k <= last) atomicAdd(&hist[(k - base) >> shift], 1);
         }
         __syncthreads();
         int above;
-        const int bin = find_bin(hist, kSelectBins, need, &above, red, two);
+        const int bin = find_bin<kThreads, kSelectBins>(hist, need, &above, red, two);
         const int in_bin = hist[bin];
         need -= above;
         base += static_cast<uint32_t>(bin) << shift;
@@ -742,7 +761,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
         if (last - base > width) last = base + width;
         if (shift == 0 || in_bin <= 8) break;
         __syncthreads();
-        for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
+        for (int i = tid; i < kSelectBins; i += kThreads) hist[i] = 0;
         __syncthreads();
       }
       t_lo = unkey32(base);
@@ -755,7 +774,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
     // t_hi + eps, and likewise at least t_lo - eps.
     const float in_above = bounded ? t_hi + 2.f * eps : INFINITY;
     const float out_below = bounded ? t_lo - 2.f * eps : -INFINITY;
-    for (int j0 = 0; j0 < words * 32; j0 += kSelectThreads) {
+    for (int j0 = 0; j0 < words * 32; j0 += kThreads) {
       const int j = j0 + tid;
       bool in = false, near = false;
       if (j >= c0 && j < c1) {
@@ -778,13 +797,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
 
     if (n_near <= kSelectFine) {
       if (n_near > need) {
-        for (int i = warp; i < n_near; i += kSelectWarps) {
-          const uint64_t k = fine_key<T, D, G>(a, b, g, fine_at[i]);
+        for (int i = warp; i < n_near; i += kWarps) {
+          const uint64_t k = fine_key<T, D, G>(a, q_fine, b, g, fine_at[i]);
           if (lane == 0) fine[i] = k;
         }
         __syncthreads();
       }
-      for (int i = tid; i < n_near; i += kSelectThreads) {
+      for (int i = tid; i < n_near; i += kThreads) {
         const int j = fine_at[i];
         int rank_of = 0;
         if (n_near > need) {
@@ -797,19 +816,19 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
       // many blocks within the error of the border (equal keys, infinities):
       // 64-bit keys in the workspace and a radix selection over them
       uint64_t* keys = a.fine + row * a.max_blocks;
-      for (int j = c0 + warp; j < c1; j += kSelectWarps) {
+      for (int j = c0 + warp; j < c1; j += kWarps) {
         const float s = scores[j];
         if (bounded && (s > in_above || s < out_below)) continue;
-        const uint64_t k = fine_key<T, D, G>(a, b, g, j);
+        const uint64_t k = fine_key<T, D, G>(a, q_fine, b, g, j);
         if (lane == 0) keys[j] = k;
       }
       __syncthreads();
       uint64_t prefix = 0;
       int left = need;
       for (int shift = 56; shift >= 0; shift -= 8) {
-        hist[tid] = 0;  // kSelectThreads bins, 256 of them in use
+        for (int i = tid; i < kSelectBins; i += kThreads) hist[i] = 0;  // 256 of them in use
         __syncthreads();
-        for (int j = c0 + tid; j < c1; j += kSelectThreads) {
+        for (int j = c0 + tid; j < c1; j += kThreads) {
           const float s = scores[j];
           if (bounded && (s > in_above || s < out_below)) continue;
           const uint64_t k = keys[j];
@@ -817,14 +836,14 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
         }
         __syncthreads();
         int above;
-        const int bin = find_bin(hist, kSelectThreads, left, &above, red, two);
+        const int bin = find_bin<kThreads, kSelectBins>(hist, left, &above, red, two);
         left -= above;
         prefix |= static_cast<uint64_t>(bin) << shift;
         __syncthreads();
       }
       // keys above `prefix`, and the first `left` equal to it
       int equal = 0;
-      for (int j0 = 0; j0 < words * 32; j0 += kSelectThreads) {
+      for (int j0 = 0; j0 < words * 32; j0 += kThreads) {
         const int j = j0 + tid;
         bool in = false, eq = false;
         if (j >= c0 && j < c1) {
@@ -840,7 +859,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
         __syncthreads();
         int before = equal + __popc(me & ((1u << lane) - 1));
 #pragma unroll
-        for (int w = 0; w < kSelectWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           if (w < warp) before += red[w];
           equal += red[w];
         }
@@ -853,7 +872,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
 
   // ---- the bitmap as an ascending list ----
   int done = 0;
-  for (int w0 = 0; w0 < words; w0 += kSelectThreads) {
+  for (int w0 = 0; w0 < words; w0 += kThreads) {
     const int w = w0 + tid;
     uint32_t m = w < words ? bitmap[w] : 0;
     const int n = __popc(m);
@@ -868,7 +887,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
     __syncthreads();
     at += done - n;
 #pragma unroll
-    for (int x = 0; x < kSelectWarps; ++x) {
+    for (int x = 0; x < kWarps; ++x) {
       if (x < warp) at += red[x];
       done += red[x];
     }

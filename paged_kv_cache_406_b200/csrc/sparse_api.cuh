@@ -60,11 +60,14 @@ int launch_select(pkv::SelectArgs a, const char* fn, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  auto kern = pkv::select_kernel<T, D, G>;
+  const bool wide = rows <= sm_count(dev) && a.max_blocks > 2048;
+  auto kern = wide ? pkv::select_kernel<T, D, G, 1024> : pkv::select_kernel<T, D, G, 256>;
   static std::atomic<bool> opted[kMaxDevices];
   if (dev >= kMaxDevices || !opted[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSelectBlocks / 8));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select)");
+    for (auto k : {pkv::select_kernel<T, D, G, 256>, pkv::select_kernel<T, D, G, 1024>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSelectBlocks / 8));
+      if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select)");
+    }
     if (dev < kMaxDevices) opted[dev].store(true, std::memory_order_relaxed);
   }
   if (a.max_blocks > a.max_selected && a.max_selected > a.n_first + a.n_last) {  // else no score decides
@@ -75,7 +78,7 @@ int launch_select(pkv::SelectArgs a, const char* fn, cudaStream_t s) {
   }
   a.smem_scores = a.max_blocks <= kSelectSmemScores ? a.max_blocks : 0;
   const size_t smem = static_cast<size_t>((a.max_blocks + 31) / 32 + a.smem_scores) * 4;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(pkv::kSelectThreads), smem, s, a);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(wide ? 1024 : 256), smem, s, a);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return pkv::ok();
 }
