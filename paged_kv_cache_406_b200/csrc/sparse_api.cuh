@@ -106,6 +106,48 @@ SparseLayout sparse_layout(int64_t rows, int32_t group, int32_t head_dim, int32_
   return w;
 }
 
+template <typename T, int D, int G>
+int launch_sparse(const pkv::SparseDecodeArgs& a, const char* fn, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int64_t rows = int64_t(a.s.num_seqs) * a.s.num_kv_heads;
+  const int64_t chunks = (int64_t(a.s.max_selected) * a.s.block_size + 15) / 16;
+  int ctas = 1;  // as many as are resident at once (two an SM) and have a chunk for each warp
+  while (ctas < pkv::kSparseCluster && rows * ctas <= sm_count(dev) && chunks >= 2 * ctas * pkv::kSparseWarps) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
+  cfg.blockDim = dim3(pkv::kSparseThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, pkv::sparse_decode_kernel<T, D, G>, a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return pkv::ok();
+}
+
+template <typename T, int D>
+int launch_sparse_group(const pkv::SparseDecodeArgs& a, int32_t group, const char* fn, cudaStream_t s) {
+  switch (group) {
+    case 1: return launch_sparse<T, D, 1>(a, fn, s);
+    case 2: return launch_sparse<T, D, 2>(a, fn, s);
+    case 4: return launch_sparse<T, D, 4>(a, fn, s);
+    default: return launch_sparse<T, D, 8>(a, fn, s);
+  }
+}
+
+// The cluster kernel keeps a row's list in shared memory; 32-bit pools and
+// longer lists run the dense kernels on the selection as a batch of its own.
+bool sparse_by_cluster(int32_t dtype, int32_t max_selected) {
+  return dtype != PKV_F32 && max_selected <= pkv::kSparseList;
+}
+
 int sparse_decode(const char* fn, const void* q, const void* k_pool, const void* v_pool, const int32_t* block_tables,
                   const int32_t* seq_lens, const int32_t* selected, int32_t max_selected, int32_t num_seqs,
                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t max_blocks,
@@ -123,19 +165,35 @@ int sparse_decode(const char* fn, const void* q, const void* k_pool, const void*
   if (int64_t(num_blocks) * num_kv_heads * block_size > INT32_MAX)
     return fail(PKV_ERR_INVALID_ARG, "%s: pool has more than 2^31 token rows", fn);
   if (num_seqs == 0) return pkv::ok();
-  if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !selected || !workspace || !out)
+  if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !selected || !out)
     return fail(PKV_ERR_INVALID_ARG, "%s: NULL pointer", fn);
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
     return fail(PKV_ERR_INVALID_ARG, "%s: q, pools and out must be 16-byte aligned", fn);
+  const int32_t rows = num_seqs * num_kv_heads, group = num_q_heads / num_kv_heads;
+  const pkv::SparseArgs a{selected, block_tables, seq_lens, num_seqs, num_kv_heads, max_selected, max_blocks,
+                          num_blocks, block_size};
+  if (sparse_by_cluster(dtype, max_selected)) {
+    const double k = dtype == PKV_FP8_E4M3 ? k_scale : 1.0;
+    const pkv::SparseDecodeArgs d{a, q, k_pool, v_pool, out,
+                                  static_cast<float>(static_cast<double>(scale) * k * 1.4426950408889634), v_scale};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool d128 = head_dim == 128;
+    switch (dtype) {
+      case PKV_BF16:
+        return d128 ? launch_sparse_group<__nv_bfloat16, 128>(d, group, fn, s)
+                    : launch_sparse_group<__nv_bfloat16, 64>(d, group, fn, s);
+      case PKV_F16:
+        return d128 ? launch_sparse_group<__half, 128>(d, group, fn, s) : launch_sparse_group<__half, 64>(d, group, fn, s);
+      default: return launch_sparse_group<pkv::E4m3, 128>(d, group, fn, s);
+    }
+  }
+  if (!workspace) return fail(PKV_ERR_INVALID_ARG, "%s: NULL pointer", fn);
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(PKV_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
-  const int32_t rows = num_seqs * num_kv_heads, group = num_q_heads / num_kv_heads;
   const SparseLayout w = sparse_layout(rows, group, head_dim, max_selected, block_size, kAutoPartitionTokens);
   if (workspace_bytes < w.total)
     return fail(PKV_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, w.total);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  const pkv::SparseArgs a{selected, block_tables, seq_lens, num_seqs, num_kv_heads, max_selected, max_blocks,
-                          num_blocks, block_size};
   int32_t* tables = reinterpret_cast<int32_t*>(ws);
   int32_t* lens = reinterpret_cast<int32_t*>(ws + w.lens);
   cudaError_t e = launch_pdl(pkv::expand_selection_kernel, dim3(static_cast<unsigned>((int64_t(rows) + 7) / 8)),

@@ -3,6 +3,7 @@
 // selected[b][g][...] (ascending logical indices, -1 after the last) only.
 #pragma once
 
+#include "block_select.cuh"
 #include "decode.cuh"
 #include "device_common.cuh"
 
@@ -60,6 +61,336 @@ __global__ void __launch_bounds__(256) expand_selection_kernel(const SparseArgs 
     return;
   }
   if (lane == 0) lens[row] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit and e4m3 pools: a cluster of CTAs per (sequence, KV head).
+//
+// Bytes bound it: the K and V rows of the selected blocks, read once.  All
+// rows of a batch have about the same work and far less of it than dense
+// decode's, so nothing is planned: the warps of the row's cluster take its
+// 16-token chunks in turn, each with its own online softmax, and the cluster
+// joins them through distributed shared memory.
+//
+// A warp holds a chunk in registers, loaded from the pool as it is used:
+//     S[8 heads][16 tokens]   = Q[8 (of 16)][D] . K^T        (two 8-token tiles)
+//     O^T[D][8 heads]        += V^T[D][16 tokens] . P^T[16][8]
+// Lane (q, t) = (lane / 4, lane % 4) loads 16-byte pieces of K rows q and
+// q + 8, which are B fragments of S in a channel order that Q's fragments
+// share, and of V rows 2t, 2t + 1, 2t + 8, 2t + 9, whose halves exchanged
+// (prmt) are A fragments of O^T in an order of channels undone at the end.
+// S leaves each lane with head q at tokens 2t, 2t + 1, 2t + 8, 2t + 9: P's B
+// fragments as they are.  The next chunk's K is loaded when S is done, its V
+// when O is.  P enters as a sum of two f16 or three bf16 values (22 or 24
+// bits), so its rounding does not show in a 32-bit result.
+// ---------------------------------------------------------------------------
+constexpr int kSparseWarps = 8;
+constexpr int kSparseThreads = kSparseWarps * 32;
+constexpr int kSparseList = 1024;   // most selected blocks (their tiles lie in shared memory)
+constexpr int kSparseCluster = 8;
+
+struct SparseDecodeArgs {
+  SparseArgs s;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  float* out;
+  float scale_log2, v_scale;
+};
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const SparseDecodeArgs a) {
+  using Q = typename QueryOf<T>::type;
+  constexpr bool kFp8 = sizeof(T) == 1;
+  constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes
+  constexpr int kKP = kRow / 64, kVP = kRow / 128;       // pieces of a K row (four lanes) and a V row (eight lanes)
+  constexpr int kSteps = kFp8 ? 4 : 2;                   // mma steps of a K piece
+  constexpr int kTiles = kFp8 ? 8 : 4;                   // channel pairs of a V piece
+  constexpr int kTerms = std::is_same_v<Q, __nv_bfloat16> ? 3 : 2;
+  constexpr int kRec = (G * D + 2 * G + 3) / 4 * 4;      // O, m, l of a warp or a CTA; 16-byte aligned
+  __shared__ int32_t list[kSparseList];
+  __shared__ int32_t first_bad;
+  __shared__ __align__(16) float rec[kSparseWarps][kRec];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  uint32_t rank, ctas;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int64_t row = blockIdx.x / ctas;
+  const int b = static_cast<int>(row / a.s.num_kv_heads), g = static_cast<int>(row - static_cast<int64_t>(b) * a.s.num_kv_heads);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
+  const int bs = a.s.block_size, bs_shift = bs == 8 ? 3 : (bs == 16 ? 4 : 5), K = a.s.max_selected;
+
+  // ---- the tiles of the selected blocks ----
+  const int32_t* sel = a.s.selected + row * K;
+  const int L = a.s.seq_lens[b];
+  const bool fits = L >= 0 && L <= a.s.max_blocks * bs;
+  const int nblk = fits ? (L + bs - 1) >> bs_shift : 0;
+  if (tid == 0) {
+    first_bad = K;
+    if (!fits && rank == 0) record_error(PKV_ERR_INVALID_ARG);
+  }
+  // A fragments of Q: row gq is head gq (zero from G on, as are rows 8 .. 15)
+  uint32_t qa[kKP][kSteps][2];
+#pragma unroll
+  for (int i = 0; i < kKP; ++i)
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      uint2 w = make_uint2(0, 0);
+      if (gq < G)
+        w = *reinterpret_cast<const uint2*>(static_cast<const Q*>(a.q) + (row * G + gq) * D + (4 * i + tq) * 2 * kSteps * 2 + 4 * s);
+      qa[i][s][0] = w.x;
+      qa[i][s][1] = w.y;
+    }
+  __syncthreads();
+  for (int i = tid; i < K; i += kSparseThreads) {
+    const int j = sel[i], before = i ? sel[i - 1] : -1;
+    if (j >= 0 && j < nblk && j > before) {
+      int phys = a.s.block_tables[static_cast<int64_t>(b) * a.s.max_blocks + j];
+      if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.s.num_blocks)) {
+        phys = -1;  // recorded below if the list reaches it
+      }
+      list[i] = phys;
+    } else {
+      atomicMin(&first_bad, i);
+    }
+  }
+  __syncthreads();
+  const int n = first_bad;  // the list's length
+  if (rank == 0 && tid == 0 && n < K && sel[n] >= 0 && fits) record_error(PKV_ERR_INVALID_ARG);
+  for (int i = tid; i < n; i += kSparseThreads) {
+    if (list[i] < 0) {
+      record_error(PKV_ERR_BAD_BLOCK);
+      list[i] = 0;
+    }
+  }
+  __syncthreads();
+  const int tokens = n ? ((n - 1) << bs_shift) + min(bs, L - (sel[n - 1] << bs_shift)) : 0;
+  const int chunks = (tokens + 15) >> 4;
+
+  const unsigned char* kbase = static_cast<const unsigned char*>(a.k_pool) + (g << bs_shift) * static_cast<int64_t>(kRow);
+  const unsigned char* vbase = static_cast<const unsigned char*>(a.v_pool) + (g << bs_shift) * static_cast<int64_t>(kRow);
+  const int64_t tile_bytes = static_cast<int64_t>(a.s.num_kv_heads) * bs * kRow;
+  auto row_at = [&](int token) {  // byte offset of a token's row
+    return list[token >> bs_shift] * tile_bytes + (token & (bs - 1)) * kRow;
+  };
+  uint4 kx[2][kKP], vx[4][kVP];
+  auto load_k = [&](int c) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int token = c * 16 + gq + 8 * r;
+      const bool live = token < tokens;
+      const uint4* src = reinterpret_cast<const uint4*>(kbase + row_at(live ? token : 0)) + tq;
+#pragma unroll
+      for (int i = 0; i < kKP; ++i) kx[r][i] = live ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto load_v = [&](int c) {  // rows behind the last token are zero: whatever lies there is not read
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int token = c * 16 + 2 * tq + (r & 1) + 8 * (r >> 1);
+      const bool live = token < tokens;
+      const uint4* src = reinterpret_cast<const uint4*>(vbase + row_at(live ? token : 0)) + gq;
+#pragma unroll
+      for (int i = 0; i < kVP; ++i) vx[r][i] = live ? __ldg(src + 8 * i) : make_uint4(0, 0, 0, 0);
+    }
+  };
+
+  float acc[kVP][kTiles][4];
+#pragma unroll
+  for (int i = 0; i < kVP; ++i)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
+  float m = -INFINITY, l = 0.f;  // of head gq
+  const int step = static_cast<int>(ctas) * kSparseWarps;
+  int c = static_cast<int>(rank) * kSparseWarps + warp;
+  if (c < chunks) {
+    load_k(c);
+    load_v(c);
+  }
+  for (; c < chunks; c += step) {
+    // ---- scores ----
+    float s[2][4] = {};
+#pragma unroll
+    for (int i = 0; i < kKP; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t v[4] = {kx[r][i].x, kx[r][i].y, kx[r][i].z, kx[r][i].w};
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) {
+          const uint32_t qf[4] = {qa[i][t][0], 0u, qa[i][t][1], 0u};
+          if constexpr (kFp8) mma_16816<Q>(s[r], qf, e4m3x2_to_f16x2(v[t]), e4m3x2_to_f16x2(v[t] >> 16));
+          else mma_16816<Q>(s[r], qf, v[2 * t], v[2 * t + 1]);
+        }
+      }
+    const int nv = tokens - c * 16;  // valid tokens from the chunk's first
+    if (c + step < chunks) load_k(c + step);
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int token = 2 * tq + (k & 1) + 8 * (k >> 1);
+      x[k] = token < nv ? s[k >> 1][k & 1] * a.scale_log2 : -INFINITY;
+    }
+    // ---- online softmax (the running maximum moves only by more than the threshold) ----
+    float bm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    if (__any_sync(kFull, bm > m + kRescaleThreshold)) {
+      bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
+      bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
+      const float nm = fmaxf(m, bm), f = nm == -INFINITY ? 1.f : fast_exp2(m - nm);
+      m = nm;
+      l *= f;
+      const float f0 = __shfl_sync(kFull, f, 8 * tq), f1 = __shfl_sync(kFull, f, 8 * tq + 4);  // heads 2 tq, 2 tq + 1
+#pragma unroll
+      for (int i = 0; i < kVP; ++i)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          acc[i][t][0] *= f0;
+          acc[i][t][2] *= f0;
+          acc[i][t][1] *= f1;
+          acc[i][t][3] *= f1;
+        }
+    }
+    uint32_t pb[kTerms][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float p0 = fast_exp2(x[2 * r] - m), p1 = fast_exp2(x[2 * r + 1] - m);
+      l += p0 + p1;
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t) {
+        Chunk<Q, 2> h;
+        h.e[0] = narrow1<Q>(p0);
+        h.e[1] = narrow1<Q>(p1);
+        p0 -= widen1<Q>(h.e[0]);
+        p1 -= widen1<Q>(h.e[1]);
+        pb[t][r] = h.raw;
+      }
+    }
+    // ---- O^T += V^T . P^T ----
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) {
+      uint32_t w[4][kTiles];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t v[4] = {vx[r][i].x, vx[r][i].y, vx[r][i].z, vx[r][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (kFp8) {
+            w[r][2 * k] = e4m3x2_to_f16x2(v[k]);
+            w[r][2 * k + 1] = e4m3x2_to_f16x2(v[k] >> 16);
+          } else {
+            w[r][k] = v[k];
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        // row q: channel 2 t of the piece, row q + 8: channel 2 t + 1
+        const uint32_t f[4] = {__byte_perm(w[0][t], w[1][t], 0x5410), __byte_perm(w[0][t], w[1][t], 0x7632),
+                               __byte_perm(w[2][t], w[3][t], 0x5410), __byte_perm(w[2][t], w[3][t], 0x7632)};
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) mma_16816<Q>(acc[i][t], f, pb[k][0], pb[k][1]);
+      }
+    }
+    if (c + step < chunks) load_v(c + step);
+  }
+
+  // ---- join the warps ----
+  l += __shfl_xor_sync(kFull, l, 1);
+  l += __shfl_xor_sync(kFull, l, 2);
+  float* mine = rec[warp];
+#pragma unroll
+  for (int i = 0; i < kVP; ++i)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int d = (8 * i + gq) * 2 * kTiles + 2 * t;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (2 * tq + x < G)
+          *reinterpret_cast<float2*>(mine + (2 * tq + x) * D + d) = make_float2(acc[i][t][x], acc[i][t][2 + x]);
+    }
+  if (tq == 0 && gq < G) {
+    mine[G * D + gq] = m;
+    mine[G * D + G + gq] = l;
+  }
+  __syncthreads();
+  // the CTA's record takes the place of warp 0's: each thread rewrites only what it alone reads
+  float mh[kSparseWarps];
+  auto factors = [&](int h) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kSparseWarps; ++w) top = fmaxf(top, rec[w][G * D + h]);
+#pragma unroll
+    for (int w = 0; w < kSparseWarps; ++w) mh[w] = top == -INFINITY ? 0.f : fast_exp2(rec[w][G * D + h] - top);
+    return top;
+  };
+  for (int e = tid * 4; e < G * D; e += kSparseThreads * 4) {
+    factors(e / D);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kSparseWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(&rec[w][e]);
+      o.x += mh[w] * y.x;
+      o.y += mh[w] * y.y;
+      o.z += mh[w] * y.z;
+      o.w += mh[w] * y.w;
+    }
+    *reinterpret_cast<float4*>(&rec[0][e]) = o;
+  }
+  float cta_m = 0.f, cta_l = 0.f;
+  if (tid < G) {
+    cta_m = factors(tid);
+#pragma unroll
+    for (int w = 0; w < kSparseWarps; ++w) cta_l += mh[w] * rec[w][G * D + G + tid];
+  }
+  __syncthreads();
+  if (tid < G) {
+    rec[0][G * D + tid] = cta_m;
+    rec[0][G * D + G + tid] = cta_l;
+  }
+
+  // ---- join the CTAs: each finishes a share of the outputs ----
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  auto remote = [&](const float* p, uint32_t r) {
+    uint32_t addr;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(p)), "r"(r));
+    return addr;
+  };
+  for (int e = (static_cast<int>(rank) * kSparseThreads + tid) * 4; e < G * D; e += static_cast<int>(ctas) * kSparseThreads * 4) {
+    const int h = e / D;
+    float cm[kSparseCluster], top = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int r = 0; r < kSparseCluster; ++r) {
+      cm[r] = -INFINITY;
+      if (r < static_cast<int>(ctas))
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(cm[r]) : "r"(remote(&rec[0][G * D + h], r)) : "memory");
+      top = fmaxf(top, cm[r]);
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kSparseCluster; ++r) {
+      if (r < static_cast<int>(ctas)) {
+        float cl;
+        float4 y;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(cl) : "r"(remote(&rec[0][G * D + G + h], r)) : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                     : "r"(remote(&rec[0][e], r))
+                     : "memory");
+        const float f = top == -INFINITY ? 0.f : fast_exp2(cm[r] - top);
+        den += f * cl;
+        o.x += f * y.x;
+        o.y += f * y.y;
+        o.z += f * y.z;
+        o.w += f * y.w;
+      }
+    }
+    const float inv = den > 0.f ? a.v_scale / den : 0.f;
+    *reinterpret_cast<float4*>(a.out + row * G * D + e) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+  // no CTA leaves while another reads its record
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace pkv
