@@ -13,10 +13,14 @@
 // are 32-bit, and each output is rounded once.
 //
 // What bounds it: bytes (each element is read and written once, 3 flops per
-// rotated one).  A token's R/2 angles are computed once by its CTA and shared
-// by all its heads through shared memory; a thread then moves "units" of two
-// 16-byte chunks that hold both halves of the pairs, so a rotation needs no
-// exchange between threads and may run in place.
+// rotated one).  A CTA takes a few tokens: it issues the loads of the first
+// rows, computes the tokens' angles once for all heads under them, and shares
+// them through shared memory.  A thread keeps to one unit of every row it
+// moves, two 16-byte chunks that hold both halves of its pairs: a token's sines
+// and cosines stay in its registers, a rotation needs no exchange between
+// threads and may run in place.  A row in flight per thread and many threads
+// did better than two to four rows of fewer: 8192 tokens of 32 + 8 + 8 heads in
+// 39.5 us (5.1 TB/s) against 44 to 48, four tokens a CTA against 41.5 for one.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -27,8 +31,9 @@
 
 namespace pkv {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 128;   // 256 where a row has more than 128 units
 constexpr int kRopeMaxPairs = 512;  // channel pairs of the tokens of one CTA (shared memory: 8 bytes each)
+constexpr int kRopeMaxTokens = 32;
 
 struct RopeArgs {
   const void* q;
@@ -87,179 +92,194 @@ __device__ __forceinline__ T narrow1(float x) {
   else return __float2bfloat16_rn(x);
 }
 
-// How a row is cut into units.  Half layout: unit u < half / kVec rotates
-// chunk u with chunk u + half / kVec; the chunks from 2 half / kVec on pass
-// through in twos.  Interleaved: pairs lie inside a chunk, and unit u takes
-// chunks u and u + ceil(chunks / 2).  V rows likewise, unrotated.
-struct UnitMap {
-  int32_t chunks, rot, units;  // chunks of a row; units that pair up rotated halves; units of a row
-};
-
-template <int kVec, bool kInterleaved>
-__device__ __forceinline__ UnitMap unit_map(int head_dim, int half) {
-  UnitMap m;
-  m.chunks = head_dim / kVec;
-  m.rot = kInterleaved ? 0 : half / kVec;
-  m.units = m.rot + (m.chunks - 2 * m.rot + 1) / 2;
-  return m;
+// kVec floats as codes of T, or raw e4m3 codes.
+template <typename T, int kVec>
+__device__ __forceinline__ Chunk<T, kVec> narrow_chunk(const float (&f)[kVec]) {
+  Chunk<T, kVec> c;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) c.e[i] = narrow1<T>(f[i]);
+  return c;
+}
+template <int kVec>
+__device__ __forceinline__ Chunk<uint8_t, kVec> e4m3_chunk(const float (&f)[kVec], float scale) {
+  Chunk<uint8_t, kVec> c;
+  if constexpr (kVec == 1) {
+    c.e[0] = __nv_cvt_float_to_fp8(f[0] * scale, __NV_SATFINITE, __NV_E4M3);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+      const __nv_fp8x2_storage_t y = __nv_cvt_float2_to_fp8x2(make_float2(f[i] * scale, f[i + 1] * scale), __NV_SATFINITE, __NV_E4M3);
+      c.e[i] = static_cast<uint8_t>(y);
+      c.e[i + 1] = static_cast<uint8_t>(y >> 8);
+    }
+  }
+  return c;
 }
 
-// kPool: 0 rotates q only; 1 also appends k and v to a pool of type T;
-// 2 to an e4m3 pool.
+// kPool: 0 rotates q only; 1 also appends k and v to a pool of type T; 2 to an
+// e4m3 pool.  A row is cut into units of two kVec-element chunks: in the half
+// layout unit x < half / kVec holds chunk x and its partner x + half / kVec, the
+// others two chunks that pass through; interleaved, pairs lie inside a chunk
+// and the two are any.  V rows are cut the same way and pass through.
 template <typename T, typename TQ, int kVec, bool kInterleaved, int kPool>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
+  using C = Chunk<T, kVec>;
   __shared__ float2 cs[kRopeMaxPairs];
+  __shared__ int64_t place[kPool ? kRopeMaxTokens : 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int chunks = a.head_dim / kVec, units = (chunks + 1) / 2;
+  const int rot = kInterleaved ? 0 : a.half / kVec;  // units that rotate (half layout)
+  const int rows = a.num_q_heads + (kPool ? 2 * a.num_kv_heads : 0);
+  const int lines = blockDim.x / units;              // rows the CTA moves at a time
+  const int line = threadIdx.x / units, x = threadIdx.x - line * units;
   const int tok0 = blockIdx.x * a.tokens_per_cta;
-  const int ntok = min(a.tokens_per_cta, a.n_tokens - tok0);
-  const UnitMap rm = unit_map<kVec, kInterleaved>(a.head_dim, a.half);
-  const int vunits = (rm.chunks + 1) / 2;
-  const int q_units = a.num_q_heads * rm.units;
-  const int k_units = kPool ? a.num_kv_heads * rm.units : 0;
-  const int per_token = q_units + k_units + (kPool ? a.num_kv_heads * vunits : 0);
+  // this thread's rows: line, line + lines, ... of the tokens' rows in order;
+  // none for the threads left over
+  const int ntok = line < lines ? min(a.tokens_per_cta, a.n_tokens - tok0) : 0;
+  const int dt = lines / rows, dr = lines - dt * rows;
+  int t = line / rows, row = line - t * rows;
 
-  for (int i = threadIdx.x; i < ntok * a.half; i += kRopeThreads) {
-    const int t = i / a.half, p = i - t * a.half;
-    const double turns = static_cast<double>(a.positions[tok0 + t]) * a.inv_freq[p] * 0.15915494309189533577;
+  int c0, c1;
+  if (kInterleaved || x >= rot) {
+    c0 = 2 * rot + (x - rot);
+    c1 = c0 + (chunks - 2 * rot + 1) / 2;
+  } else {
+    c0 = x;
+    c1 = x + rot;
+  }
+  const bool two = c1 < chunks;
+  const int e0 = c0 * kVec, e1 = two ? c1 * kVec : c0 * kVec;
+
+  auto source = [&](int t, int r) {
+    const int64_t tok = tok0 + t;
+    if (!kPool || r < a.num_q_heads) return static_cast<const T*>(a.q) + tok * a.q_stride + r * a.head_dim;
+    r -= a.num_q_heads;
+    if (r < a.num_kv_heads) return static_cast<const T*>(a.k) + tok * a.k_stride + r * a.head_dim;
+    return static_cast<const T*>(a.v) + tok * a.v_stride + (r - a.num_kv_heads) * a.head_dim;
+  };
+  C x0, x1;
+  auto load = [&] {
+    if (t < ntok) {
+      const T* src = source(t, row);
+      x0.raw = *reinterpret_cast<const typename C::Raw*>(src + e0);
+      x1.raw = *reinterpret_cast<const typename C::Raw*>(src + e1);
+    }
+  };
+  load();
+
+  const int held = min(a.tokens_per_cta, a.n_tokens - tok0);
+  for (int i = threadIdx.x; i < held * a.half; i += blockDim.x) {
+    const int ti = i / a.half, p = i - ti * a.half;
+    const double turns = static_cast<double>(a.positions[tok0 + ti]) * a.inv_freq[p] * 0.15915494309189533577;
     const float r = static_cast<float>(turns - rint(turns));  // in [-0.5, 0.5]
     float s, c;
     sincospif(2.0f * r, &s, &c);
     cs[i] = make_float2(c * a.factor, s * a.factor * a.sin_sign);
   }
+  if constexpr (kPool > 0) {  // head 0's row of each token in the pools, elements; -1: none
+    for (int i = threadIdx.x; i < held; i += blockDim.x) {
+      const int32_t slot = a.slots[tok0 + i];
+      const int32_t blk = slot / a.block_size, off = slot - blk * a.block_size;
+      const bool in = slot >= 0 && blk < a.num_blocks;
+      if (slot >= 0 && !in) record_error(PKV_ERR_BAD_BLOCK);
+      place[i] = in ? (static_cast<int64_t>(blk) * a.num_kv_heads * a.block_size + off) * a.head_dim : -1;
+    }
+  }
   __syncthreads();
 
-  for (int u0 = threadIdx.x; u0 < ntok * per_token; u0 += kRopeThreads) {
-    const int t = u0 / per_token;
-    int u = u0 - t * per_token;
-    const int64_t tok = tok0 + t;
-    // which row: 0 q, 1 k, 2 v
-    int kind = 0;
-    if (kPool && u >= q_units) {
-      u -= q_units;
-      kind = 1;
-      if (u >= k_units) {
-        u -= k_units;
-        kind = 2;
+  float2 w[kVec];                // of the unit's pairs
+  const bool turn0 = kInterleaved ? e0 / 2 < a.half : x < rot;  // whether its chunks hold rotated channels
+  const bool turn1 = kInterleaved ? two && e1 / 2 < a.half : turn0;
+  int at = -1;                   // the token that w is of
+  while (t < ntok) {
+    const int kind = !kPool || row < a.num_q_heads ? 0 : (row < a.num_q_heads + a.num_kv_heads ? 1 : 2);
+    const int64_t dst = kPool && kind ? place[t] : 0;
+    if (at != t) {
+      at = t;
+      const float2* tc = cs + t * a.half;
+      if constexpr (kInterleaved) {  // a chunk may be rotated in part
+#pragma unroll
+        for (int i = 0; i < kVec / 2; ++i) {
+          if (turn0 && e0 / 2 + i < a.half) w[i] = tc[e0 / 2 + i];
+          if (turn1 && e1 / 2 + i < a.half) w[kVec / 2 + i] = tc[e1 / 2 + i];
+        }
+      } else if (turn0) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w[i] = tc[e0 + i];
       }
     }
-    const int units = kind == 2 ? vunits : rm.units;
-    const int h = u / units;
-    u -= h * units;
-    int c0, c1;
-    bool rotate;
-    if (kind == 2 || kInterleaved) {
-      c0 = u;
-      c1 = u + (rm.chunks + 1) / 2;
-      rotate = kInterleaved && kind != 2;
-    } else if (u < rm.rot) {
-      c0 = u;
-      c1 = u + rm.rot;
-      rotate = true;
-    } else {
-      const int rest = rm.chunks - 2 * rm.rot;
-      c0 = 2 * rm.rot + (u - rm.rot);
-      c1 = c0 + (rest + 1) / 2;
-      rotate = false;
-    }
-    const bool two = c1 < rm.chunks;
-    int64_t dst = 0;  // of the row in its pool, elements
-    if (kPool && kind) {
-      const int32_t slot = a.slots[tok];
-      if (slot < 0) continue;
-      const int32_t blk = slot / a.block_size, off = slot - blk * a.block_size;
-      if (blk >= a.num_blocks) {
-        if (kind == 1 && h == 0 && u == 0) record_error(PKV_ERR_BAD_BLOCK);
-        continue;
-      }
-      dst = ((static_cast<int64_t>(blk) * a.num_kv_heads + h) * a.block_size + off) * a.head_dim;
-    }
-    using C = Chunk<T, kVec>;
-    const T* src = kind == 0 ? static_cast<const T*>(a.q) + tok * a.q_stride
-                             : (kind == 1 ? static_cast<const T*>(a.k) + tok * a.k_stride
-                                          : static_cast<const T*>(a.v) + tok * a.v_stride);
-    src += h * a.head_dim;
-    C x0, x1;
-    x0.raw = *reinterpret_cast<const typename C::Raw*>(src + c0 * kVec);
-    if (two) x1.raw = *reinterpret_cast<const typename C::Raw*>(src + c1 * kVec);
-    else x1 = x0;
-
     float f0[kVec], f1[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       f0[i] = widen1<T>(x0.e[i]);
       f1[i] = widen1<T>(x1.e[i]);
     }
-    if (rotate) {
-      const float2* tc = cs + t * a.half;
+    if (kind != 2) {
       if constexpr (kInterleaved) {
 #pragma unroll
-        for (int i = 0; i < kVec; i += 2) {
-          const int p0 = (c0 * kVec + i) >> 1, p1 = (c1 * kVec + i) >> 1;
-          if (p0 < a.half) {
-            const float2 w = tc[p0];
-            const float xa = f0[i], xb = f0[i + 1];
-            f0[i] = xa * w.x - xb * w.y;
-            f0[i + 1] = xa * w.y + xb * w.x;
-            x0.e[i] = narrow1<T>(f0[i]);
-            x0.e[i + 1] = narrow1<T>(f0[i + 1]);
+        for (int i = 0; i < kVec / 2; ++i) {
+          if (turn0 && e0 / 2 + i < a.half) {
+            const float xa = f0[2 * i], xb = f0[2 * i + 1];
+            f0[2 * i] = xa * w[i].x - xb * w[i].y;
+            f0[2 * i + 1] = xa * w[i].y + xb * w[i].x;
+            x0.e[2 * i] = narrow1<T>(f0[2 * i]);
+            x0.e[2 * i + 1] = narrow1<T>(f0[2 * i + 1]);
           }
-          if (two && p1 < a.half) {
-            const float2 w = tc[p1];
-            const float xa = f1[i], xb = f1[i + 1];
-            f1[i] = xa * w.x - xb * w.y;
-            f1[i + 1] = xa * w.y + xb * w.x;
-            x1.e[i] = narrow1<T>(f1[i]);
-            x1.e[i + 1] = narrow1<T>(f1[i + 1]);
+          if (turn1 && e1 / 2 + i < a.half) {
+            const float2 v = w[kVec / 2 + i];
+            const float xa = f1[2 * i], xb = f1[2 * i + 1];
+            f1[2 * i] = xa * v.x - xb * v.y;
+            f1[2 * i + 1] = xa * v.y + xb * v.x;
+            x1.e[2 * i] = narrow1<T>(f1[2 * i]);
+            x1.e[2 * i + 1] = narrow1<T>(f1[2 * i + 1]);
           }
         }
-      } else {
+      } else if (turn0) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-          const float2 w = tc[c0 * kVec + i];
           const float xa = f0[i], xb = f1[i];
-          f0[i] = xa * w.x - xb * w.y;
-          f1[i] = xa * w.y + xb * w.x;
-          x0.e[i] = narrow1<T>(f0[i]);
-          x1.e[i] = narrow1<T>(f1[i]);
+          f0[i] = xa * w[i].x - xb * w[i].y;
+          f1[i] = xa * w[i].y + xb * w[i].x;
         }
+        x0 = narrow_chunk<T, kVec>(f0);
+        x1 = narrow_chunk<T, kVec>(f1);
       }
     }
-
-    if (kind == 0) {
-      TQ* out = static_cast<TQ*>(a.q_out) + tok * a.out_stride + h * a.head_dim;
+    if (dst < 0) {
+      // a padding token's K and V go nowhere
+    } else if (kind == 0) {
+      TQ* out = static_cast<TQ*>(a.q_out) + (tok0 + static_cast<int64_t>(t)) * a.out_stride + row * a.head_dim;
       if constexpr (std::is_same_v<T, TQ>) {  // channels that pass through keep their bits
-        *reinterpret_cast<typename C::Raw*>(out + c0 * kVec) = x0.raw;
-        if (two) *reinterpret_cast<typename C::Raw*>(out + c1 * kVec) = x1.raw;
+        *reinterpret_cast<typename C::Raw*>(out + e0) = x0.raw;
+        if (two) *reinterpret_cast<typename C::Raw*>(out + e1) = x1.raw;
       } else {
         using CQ = Chunk<TQ, kVec>;
-        CQ y0, y1;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          y0.e[i] = narrow1<TQ>(f0[i]);
-          y1.e[i] = narrow1<TQ>(f1[i]);
-        }
-        *reinterpret_cast<typename CQ::Raw*>(out + c0 * kVec) = y0.raw;
-        if (two) *reinterpret_cast<typename CQ::Raw*>(out + c1 * kVec) = y1.raw;
+        *reinterpret_cast<typename CQ::Raw*>(out + e0) = narrow_chunk<TQ, kVec>(f0).raw;
+        if (two) *reinterpret_cast<typename CQ::Raw*>(out + e1) = narrow_chunk<TQ, kVec>(f1).raw;
       }
-    } else if constexpr (kPool == 1) {
-      T* out = static_cast<T*>(kind == 1 ? a.k_pool : a.v_pool) + dst;
-      *reinterpret_cast<typename C::Raw*>(out + c0 * kVec) = x0.raw;
-      if (two) *reinterpret_cast<typename C::Raw*>(out + c1 * kVec) = x1.raw;
-    } else if constexpr (kPool == 2) {
-      // the rotated value is rounded once, straight to its e4m3 code
-      uint8_t* out = static_cast<uint8_t*>(kind == 1 ? a.k_pool : a.v_pool) + dst;
-      const float inv = kind == 1 ? a.k_inv : a.v_inv;
-      using C8 = Chunk<uint8_t, kVec>;
-      C8 y0, y1;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        y0.e[i] = __nv_cvt_float_to_fp8(f0[i] * inv, __NV_SATFINITE, __NV_E4M3);
-        y1.e[i] = __nv_cvt_float_to_fp8(f1[i] * inv, __NV_SATFINITE, __NV_E4M3);
+    } else if constexpr (kPool > 0) {
+      const int h = row - a.num_q_heads - (kind == 2 ? a.num_kv_heads : 0);
+      const int64_t to = dst + static_cast<int64_t>(h) * a.block_size * a.head_dim;
+      if constexpr (kPool == 1) {
+        T* out = static_cast<T*>(kind == 1 ? a.k_pool : a.v_pool) + to;
+        *reinterpret_cast<typename C::Raw*>(out + e0) = x0.raw;
+        if (two) *reinterpret_cast<typename C::Raw*>(out + e1) = x1.raw;
+      } else {  // the rotated value is rounded once, straight to its e4m3 code
+        using C8 = Chunk<uint8_t, kVec>;
+        uint8_t* out = static_cast<uint8_t*>(kind == 1 ? a.k_pool : a.v_pool) + to;
+        const float inv = kind == 1 ? a.k_inv : a.v_inv;
+        *reinterpret_cast<typename C8::Raw*>(out + e0) = e4m3_chunk<kVec>(f0, inv).raw;
+        if (two) *reinterpret_cast<typename C8::Raw*>(out + e1) = e4m3_chunk<kVec>(f1, inv).raw;
       }
-      *reinterpret_cast<typename C8::Raw*>(out + c0 * kVec) = y0.raw;
-      if (two) *reinterpret_cast<typename C8::Raw*>(out + c1 * kVec) = y1.raw;
     }
+    t += dt;
+    row += dr;
+    if (row >= rows) {
+      row -= rows;
+      ++t;
+    }
+    load();
   }
 }
 

@@ -33,13 +33,19 @@ template <typename T, typename TQ, int kPool>
 int launch_rope(pkv::RopeArgs a, bool interleaved, const char* fn, cudaStream_t s) {
   constexpr int kVec = 16 / sizeof(T);
   const bool vec = interleaved || a.half % kVec == 0;
-  const int row_units = interleaved || !vec ? a.head_dim / (vec ? 2 * kVec : 2) : a.head_dim / (2 * kVec);
-  const int64_t per_token = static_cast<int64_t>(a.num_q_heads + (kPool ? 2 * a.num_kv_heads : 0)) * row_units;
-  a.tokens_per_cta =
-      static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(1, per_token),
-                                                                   pkv::kRopeMaxPairs / a.half)));
-  const dim3 grid(static_cast<unsigned>((a.n_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta)), block(pkv::kRopeThreads);
-  cudaError_t e;
+  const int chunks = a.head_dim / (vec ? kVec : 1), units = (chunks + 1) / 2;
+  const int rows = a.num_q_heads + (kPool ? 2 * a.num_kv_heads : 0);
+  const int threads = units > pkv::kRopeThreads ? 2 * pkv::kRopeThreads : pkv::kRopeThreads;
+  // tokens of a CTA: what fills its lines, and more where there are enough for
+  // eight CTAs an SM all the same
+  const int lines = threads / units;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int want = std::max(std::max(1, lines / rows), std::min(4, a.n_tokens / (8 * sm_count(dev))));
+  a.tokens_per_cta = std::min(std::min(want, pkv::kRopeMaxTokens), std::max(1, pkv::kRopeMaxPairs / a.half));
+  const dim3 grid(static_cast<unsigned>((a.n_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta)),
+      block(static_cast<unsigned>(threads));
   if (interleaved) e = launch_pdl(pkv::rope_kernel<T, TQ, kVec, true, kPool>, grid, block, 0, s, a);
   else if (vec) e = launch_pdl(pkv::rope_kernel<T, TQ, kVec, false, kPool>, grid, block, 0, s, a);
   else e = launch_pdl(pkv::rope_kernel<T, TQ, 1, false, kPool>, grid, block, 0, s, a);

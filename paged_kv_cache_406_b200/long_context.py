@@ -8,6 +8,7 @@ need not be the current one.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -17,13 +18,14 @@ from ._native import check, lib
 from .binding import _DTYPES, _dtype_code
 
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
 
 
 def _issue(fn, dev: int, *args) -> None:
     """One library call on ``dev`` and the stream current there."""
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch._C._cuda_getDevice():
+    stream = _raw_stream(dev)
+    if dev == _current_device():
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -32,24 +34,32 @@ def _issue(fn, dev: int, *args) -> None:
         check(rc)
 
 
-def _on(t: torch.Tensor, name: str, dev: Optional[int] = None, dtype=None, packed: bool = True) -> int:
-    """Checks a tensor; returns its device's index."""
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of a CUDA tensor's device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if packed and not t.is_contiguous():
+    return t.get_device()
+
+
+def _on(t: torch.Tensor, name: str, dev: int, dtype=None) -> None:
+    """Checks that a tensor is packed, on device ``dev`` and of ``dtype``."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous() and (
+            dtype is None or t.dtype == dtype):
+        return
+    if _device(t, name) != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the other tensors are on device {dev}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    d = t.get_device()
-    if dev is not None and d != dev:
-        raise ValueError(f"{name} is on device {d}, the other tensors are on device {dev}")
-    return d
+    raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def _rows(t: torch.Tensor, name: str, dev: Optional[int], dtype=None):
+def _rows(t: torch.Tensor, name: str, dev: int, dtype=None):
     """Checks ``[n_tokens, heads, head_dim]`` with packed heads; returns its
     sizes and the token stride."""
-    _on(t, name, dev, dtype, packed=False)
+    if _device(t, name) != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the other tensors are on device {dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
     n, heads, d = t.shape
@@ -97,8 +107,8 @@ def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
     stride) by ``positions * inv_freq``; returns ``out`` (``x`` itself for in
     place).  ``transpose`` applies the transposed map, which takes the
     gradient of the result to that of ``x``."""
-    n, heads, d, stride = _rows(x, "x", None)
-    dev = x.get_device()
+    dev = _device(x, "x")
+    n, heads, d, stride = _rows(x, "x", dev)
     rot = _positions(positions, inv_freq, n, dev)
     if x.dtype not in _DTYPES or x.dtype in _E4M3:
         raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
@@ -115,8 +125,8 @@ def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
 
 
 def _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, q_dtype):
-    n, hkv, d, ks = _rows(k, "k", None)
-    dev = k.get_device()
+    dev = _device(k, "k")
+    n, hkv, d, ks = _rows(k, "k", dev)
     n2, hkv2, d2, vs = _rows(v, "v", dev, k.dtype)
     nq, hq, dq, qs = _rows(q, "q", dev, k.dtype)
     nb, ph, bs, pd = _pools(k_pool, v_pool, dev)
@@ -189,7 +199,8 @@ def pkv_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens:
     pool's dtype), the smallest and largest key of every block that holds one
     of the last ``new_tokens`` tokens of a sequence (int32 ``[num_seqs]``;
     None: one each); returns ``bounds``."""
-    dev = _on(k_pool, "k_pool")
+    dev = _device(k_pool, "k_pool")
+    _on(k_pool, "k_pool", dev)
     if k_pool.dim() != 4:
         raise ValueError("k_pool must be [num_blocks, num_kv_heads, block_size, head_dim]")
     nb, hkv, bs, d = k_pool.shape
@@ -207,6 +218,7 @@ def pkv_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens:
     return bounds
 
 
+@functools.lru_cache(maxsize=256)
 def pkv_select_workspace_size(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int) -> int:
     """Workspace bytes of :func:`pkv_block_select`."""
     out = ctypes.c_size_t(0)
@@ -222,7 +234,8 @@ def pkv_block_select(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.
     ``[num_seqs, num_kv_heads, max_selected]``, ascending logical block
     indices, -1 behind the last - the first ``n_first`` and last ``n_last``
     blocks and the best-scored of the others (see the C declaration)."""
-    dev = _on(bounds, "bounds")
+    dev = _device(bounds, "bounds")
+    _on(bounds, "bounds", dev)
     if bounds.dim() != 4 or bounds.shape[2] != 2:
         raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
     nb, hkv, _, d = bounds.shape
@@ -246,6 +259,7 @@ def pkv_block_select(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.
     return selected
 
 
+@functools.lru_cache(maxsize=256)
 def pkv_sparse_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_selected: int,
                               block_size: int, dtype: torch.dtype) -> int:
     """Workspace bytes of the block-sparse decode over pools of ``dtype``."""
@@ -256,7 +270,7 @@ def pkv_sparse_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int
 
 
 def _sparse(fn, q, k_pool, v_pool, block_tables, seq_lens, selected, tail, q_dtype, out, workspace):
-    dev = _on(k_pool, "k_pool")
+    dev = _device(k_pool, "k_pool")
     nb, hkv, bs, d = _pools(k_pool, v_pool, dev)
     b, maxb = _batch(block_tables, seq_lens, dev)
     _on(q, "q", dev, q_dtype)
