@@ -611,7 +611,9 @@ int pkv_block_select(const void* q, const void* bounds, const int32_t* block_tab
                      int32_t n_first, int32_t n_last, int32_t dtype, void* workspace, size_t workspace_bytes,
                      int32_t* selected, void* stream);
 
-/* Bytes of device workspace the block-sparse decode needs.  Host only. */
+/* Bytes of device workspace the block-sparse decode needs: 0 for 16-bit and
+ * e4m3 pools with max_selected up to 1024 (workspace may then be NULL).  Host
+ * only. */
 int pkv_sparse_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                               int32_t max_selected, int32_t block_size, int32_t dtype, size_t* bytes);
 

@@ -333,8 +333,10 @@ extern "C" int pkv_sparse_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
   if (rc) return rc;
   if (max_selected <= 0 || int64_t(max_selected) * block_size > (int64_t(1) << 30))
     return fail(PKV_ERR_INVALID_ARG, "%s: max_selected %d", fn, max_selected);
-  *bytes = std::max<size_t>(256, sparse_layout(int64_t(num_seqs) * num_kv_heads, num_q_heads / num_kv_heads, head_dim,
-                                               max_selected, block_size, kAutoPartitionTokens).total);
+  *bytes = sparse_by_cluster(dtype, max_selected)
+               ? 0
+               : sparse_layout(int64_t(num_seqs) * num_kv_heads, num_q_heads / num_kv_heads, head_dim, max_selected,
+                               block_size, kAutoPartitionTokens).total;
   return pkv::ok();
 }
 

@@ -113,7 +113,7 @@ def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
     if x.dtype not in _DTYPES or x.dtype in _E4M3:
         raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
     if out is None:
-        out = torch.empty((n, heads, d), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
         ostride = heads * d
     else:
         on, oheads, od, ostride = _rows(out, "out", dev, x.dtype)
@@ -127,22 +127,28 @@ def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
 def _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, q_dtype):
     dev = _device(k, "k")
     n, hkv, d, ks = _rows(k, "k", dev)
-    n2, hkv2, d2, vs = _rows(v, "v", dev, k.dtype)
-    nq, hq, dq, qs = _rows(q, "q", dev, k.dtype)
+    dtype = k.dtype
+    if v.shape == k.shape and v.stride() == k.stride() and v.dtype == dtype and v.get_device() == dev:
+        vs = ks  # laid out as k is
+    else:
+        n2, hkv2, d2, vs = _rows(v, "v", dev, dtype)
+        if (n2, hkv2, d2) != (n, hkv, d):
+            raise ValueError("k and v differ in shape")
+    nq, hq, dq, qs = _rows(q, "q", dev, dtype)
     nb, ph, bs, pd = _pools(k_pool, v_pool, dev)
-    if (n2, hkv2, d2) != (n, hkv, d) or (nq, dq) != (n, d) or (ph, pd) != (hkv, d):
+    if nq != n or dq != d or ph != hkv or pd != d:
         raise ValueError(f"q, k, v must be [n_tokens, heads, {pd}] with {ph} heads in k and v")
     rot = _positions(positions, inv_freq, n, dev)
     _on(slot_mapping, "slot_mapping", dev, torch.int32)
     if slot_mapping.numel() != n:
         raise ValueError("slot_mapping must hold one slot per new token")
-    if k.dtype not in _DTYPES or k.dtype in _E4M3:
-        raise TypeError(f"q, k, v must be float32, bfloat16 or float16, got {k.dtype}")
+    if dtype not in _DTYPES or dtype in _E4M3:
+        raise TypeError(f"q, k, v must be float32, bfloat16 or float16, got {dtype}")
     if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=q_dtype, device=k.device)
+        q_out = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
     else:
         _on(q_out, "q_out", dev, q_dtype)
-        if tuple(q_out.shape) != (n, hq, d):
+        if q_out.shape != q.shape:
             raise ValueError("q_out has the wrong shape")
         if n and q_out.data_ptr() == q.data_ptr():
             raise ValueError("q_out must not be q")
@@ -244,25 +250,28 @@ def pkv_block_select(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.
     if q.dim() != 3 or q.shape[0] != b or q.shape[2] != d:
         raise ValueError(f"q must be [{b}, num_q_heads, {d}]")
     if selected is None:
-        selected = torch.empty((b, hkv, max_selected), dtype=torch.int32, device=q.device)
+        selected = seq_lens.new_empty((b, hkv, max_selected))
     else:
         _on(selected, "selected", dev, torch.int32)
         if tuple(selected.shape) != (b, hkv, max_selected):
             raise ValueError("selected has the wrong shape")
     if workspace is None:
-        workspace = torch.empty(pkv_select_workspace_size(b, hkv, maxb), dtype=torch.uint8, device=q.device)
+        ws_bytes = pkv_select_workspace_size(b, hkv, maxb)  # a multiple of 256
+        workspace = seq_lens.new_empty(ws_bytes // 4)
     else:
         _on(workspace, "workspace", dev, torch.uint8)
+        ws_bytes = workspace.numel()
     _issue(lib().pkv_block_select, dev, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), b,
            q.shape[1], hkv, d, nb, maxb, int(block_size), int(max_selected), int(n_first), int(n_last),
-           _dtype_code(bounds), workspace.data_ptr(), workspace.numel(), selected.data_ptr())
+           _dtype_code(bounds), workspace.data_ptr(), ws_bytes, selected.data_ptr())
     return selected
 
 
 @functools.lru_cache(maxsize=256)
 def pkv_sparse_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_selected: int,
                               block_size: int, dtype: torch.dtype) -> int:
-    """Workspace bytes of the block-sparse decode over pools of ``dtype``."""
+    """Workspace bytes of the block-sparse decode over pools of ``dtype`` (0
+    where it needs none)."""
     out = ctypes.c_size_t(0)
     check(lib().pkv_sparse_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_selected, block_size,
                                           _DTYPES[dtype], ctypes.byref(out)))
@@ -286,14 +295,17 @@ def _sparse(fn, q, k_pool, v_pool, block_tables, seq_lens, selected, tail, q_dty
         _on(out, "out", dev, torch.float32)
         if tuple(out.shape) != (b, hq, d):
             raise ValueError("out has the wrong shape")
-    if workspace is None:
-        workspace = torch.empty(pkv_sparse_workspace_size(b, hq, hkv, d, k, bs, k_pool.dtype), dtype=torch.uint8,
-                                device=q.device)
-    else:
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
         _on(workspace, "workspace", dev, torch.uint8)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    else:
+        ws_bytes = pkv_sparse_workspace_size(b, hq, hkv, d, k, bs, k_pool.dtype)  # 0 or a multiple of 256
+        if ws_bytes:
+            workspace = seq_lens.new_empty(ws_bytes // 4)
+            ws_ptr = workspace.data_ptr()
     _issue(fn, dev, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-           selected.data_ptr(), k, b, hq, hkv, d, nb, maxb, bs, *tail, workspace.data_ptr(), workspace.numel(),
-           out.data_ptr())
+           selected.data_ptr(), k, b, hq, hkv, d, nb, maxb, bs, *tail, ws_ptr, ws_bytes, out.data_ptr())
     return out
 
 

@@ -356,6 +356,25 @@ def test_sparse_decode(dtype, d, g, bs, k):
     assert bool((got.cpu()[empty] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_long_lists(dtype):
+    """More selected blocks than a CTA lists in shared memory (1024)."""
+    bs, hkv, g, d, k = 8, 2, 4, 128, 1500
+    lens = [1600 * bs - 3, 1025 * bs, 40]
+    tables, nb = batch(lens, bs, 2)
+    kp, vp = keys((nb, hkv, bs, d), dtype, 1), keys((nb, hkv, bs, d), dtype, 2)
+    q = keys((3, g * hkv, d), "f16" if dtype == "e4m3" else dtype, 3)
+    sel = choose(lens, bs, hkv, k, 5)
+    args = (q.cuda(), kp.cuda(), vp.cuda(), torch.from_numpy(tables).cuda(),
+            torch.tensor(lens, dtype=torch.int32).cuda(), torch.from_numpy(sel).cuda(), d ** -0.5)
+    got = P.pkv_paged_attention_decode_sparse_fp8(*args, 1.0, 1.0) if dtype == "e4m3" else \
+        P.pkv_paged_attention_decode_sparse(*args)
+    f = (lambda t: t.float()) if dtype == "e4m3" else (lambda t: t)
+    want = attend_by_hand(q, f(kp), f(vp), tables, lens, sel, d ** -0.5)
+    tol = TOL["f16" if dtype == "e4m3" else dtype]
+    assert bool(((got.cpu().double() - want).abs() <= tol * want.abs().clamp(min=1)).all())
+
+
 @pytest.mark.parametrize("dtype,g", [("bf16", 4), ("f16", 1), ("f32", 2)])
 def test_every_block_selected_is_dense_decode(dtype, g):
     case = Case([700, 1, 0, 64, 333], 2 * g, 2, 128, 16, dtype, seed=3)
@@ -487,8 +506,8 @@ def test_captured_steps_share_no_hidden_state():
         sel = torch.empty(3, hkv, k, dtype=torch.int32, device="cuda")
         out = torch.empty(3, g * hkv, d, device="cuda")
         ws1 = torch.empty(P.pkv_select_workspace_size(3, hkv, t.shape[1]), dtype=torch.uint8, device="cuda")
-        ws2 = torch.empty(P.pkv_sparse_workspace_size(3, g * hkv, hkv, d, k, bs, torch.bfloat16), dtype=torch.uint8,
-                          device="cuda")
+        need = P.pkv_sparse_workspace_size(3, g * hkv, hkv, d, k, bs, torch.bfloat16)
+        ws2 = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
 
         def step(kp=kp, vp=vp, bounds=bounds, q=q, t=t, L=L, sel=sel, out=out, ws1=ws1, ws2=ws2):
             P.pkv_block_bounds(kp, t, L, bounds, L, 4096)

@@ -220,8 +220,10 @@ def test_select_refusals(native, kw, code):
     (dict(hq=24), N.PKV_ERR_UNSUPPORTED),
     (dict(K=0), N.PKV_ERR_INVALID_ARG),
     (dict(scale=float("nan")), N.PKV_ERR_INVALID_ARG),
-    (dict(ws_bytes=64), N.PKV_ERR_INVALID_ARG),
-    (dict(ws=FAKE + 16), N.PKV_ERR_INVALID_ARG),
+    (dict(ws_bytes=64, K=2000), N.PKV_ERR_INVALID_ARG),     # a long list needs a workspace,
+    (dict(ws=None, K=2000), N.PKV_ERR_INVALID_ARG),
+    (dict(ws=FAKE + 16, K=2000), N.PKV_ERR_INVALID_ARG),
+    (dict(ws_bytes=64, dtype=N.PKV_F32), N.PKV_ERR_INVALID_ARG),  # and so do fp32 pools
     (dict(sel=0), N.PKV_ERR_INVALID_ARG),
     (dict(out=FAKE + 4), N.PKV_ERR_INVALID_ARG),
     (dict(nb=1 << 27), N.PKV_ERR_INVALID_ARG),           # more than 2^31 token rows
@@ -237,9 +239,9 @@ def test_sparse_decode_refusals(native, kw, code):
 
 
 def test_sparse_decode_fp8_refusals(native):
-    def call(d=128, ks=0.5, vs=0.5):
-        return native.pkv_paged_attention_decode_sparse_fp8(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 8, 2, 32, 8, d, 64, 64,
-                                                            16, 0.1, ks, vs, FAKE, 16, FAKE, None)
+    def call(d=128, ks=0.5, vs=0.5):  # a list of 2000 blocks: a workspace is needed
+        return native.pkv_paged_attention_decode_sparse_fp8(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2000, 2, 32, 8, d, 64,
+                                                            64, 16, 0.1, ks, vs, FAKE, 16, FAKE, None)
     assert call(d=64) == N.PKV_ERR_UNSUPPORTED
     assert call(ks=0.0) == N.PKV_ERR_INVALID_ARG
     assert call(vs=float("nan")) == N.PKV_ERR_INVALID_ARG
@@ -262,7 +264,9 @@ def test_workspace_sizes(native):
     assert native.pkv_select_workspace_size(64, 8, 2048, ctypes.byref(out)) == 0 and out.value >= 64 * 8 * 2048 * 12
     assert native.pkv_select_workspace_size(0, 8, 2048, ctypes.byref(out)) == 0
     assert native.pkv_select_workspace_size(1, 0, 2048, ctypes.byref(out)) == N.PKV_ERR_INVALID_ARG
-    assert native.pkv_sparse_workspace_size(64, 32, 8, 128, 64, 16, N.PKV_BF16, ctypes.byref(out)) == 0
+    assert native.pkv_sparse_workspace_size(64, 32, 8, 128, 64, 16, N.PKV_BF16, ctypes.byref(out)) == 0 and out.value == 0
+    assert native.pkv_sparse_workspace_size(64, 32, 8, 128, 64, 16, N.PKV_F32, ctypes.byref(out)) == 0 and out.value > 0
+    assert native.pkv_sparse_workspace_size(64, 32, 8, 128, 1025, 16, N.PKV_BF16, ctypes.byref(out)) == 0 and out.value > 0
     assert native.pkv_sparse_workspace_size(64, 30, 8, 128, 64, 16, N.PKV_BF16, ctypes.byref(out)) == N.PKV_ERR_INVALID_ARG
 
 
