@@ -12,27 +12,52 @@ step for one layer ("vLLM's 'memory paging' — PagedAttention illustrated", §3
 4. pkv_append_and_decode: the new tokens' K/V written into their slots by the
    launch that plans the decode, then PagedAttention decode (plus its
    partition merge) over every sequence, new token included.
+
+A cache made with ``rope`` takes q and K before their rotary rotation, which
+step 4's append then does on the way (pkv_rope_append); one made with
+``key_bounds`` keeps the bounds of each block's keys (pkv_block_bounds) and can
+attend over the best-scored blocks of each sequence only (pkv_block_select,
+pkv_paged_attention_decode_sparse): the ``max_selected`` of a decode step.
 """
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import numpy as np
 import torch
 
 from . import binding as B
+from . import long_context as LC
 from ._native import StepBuffers, check, lib
+
+
+@dataclass(frozen=True)
+class Rope:
+    """A rotary rotation: float64 frequencies on the cache's device (half as
+    many as channels are rotated), the factor of sines and cosines, and the
+    layout of the pairs.  ``Rope(*pkv_rope_frequencies(...))`` makes one."""
+    inv_freq: torch.Tensor
+    factor: float = 1.0
+    interleaved: bool = False
 
 
 class PagedKVCache:
     def __init__(self, num_blocks: int, num_kv_heads: int, head_dim: int, block_size: int,
                  dtype: torch.dtype, max_blocks_per_seq: int, device="cuda", free_order=None,
                  k_pool: Optional[torch.Tensor] = None, v_pool: Optional[torch.Tensor] = None,
-                 k_scale: float = 1.0, v_scale: float = 1.0):
+                 k_scale: float = 1.0, v_scale: float = 1.0, rope: Optional[Rope] = None, key_bounds: bool = False):
         """``dtype`` torch.float8_e4m3fn (or torch.uint8) keeps the pools as e4m3
         codes with per-pool scales ``k_scale`` / ``v_scale`` (the overview page's
-        FP8 KV cache); new rows are quantised on append and q must be float16."""
+        FP8 KV cache); new rows are quantised on append and q must be float16
+        (with ``rope`` any type that the rows have).
+
+        ``rope``: the rotation of q and K on their way in (positions are those
+        in the sequence).  ``key_bounds``: keep the bounds of every block's
+        keys, which a decode step with ``max_selected`` selects by; all rows
+        then have to come through :meth:`write_chunk` and :meth:`decode_step`,
+        or :meth:`refresh_bounds` has to follow what wrote them."""
         self.device = torch.device(device)
         self.fp8 = dtype in (torch.float8_e4m3fn, torch.uint8)
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
@@ -45,6 +70,9 @@ class PagedKVCache:
         self.v_pool = v_pool if v_pool is not None else torch.empty(shape, dtype=dtype, device=self.device)
         if tuple(self.k_pool.shape) != shape or tuple(self.v_pool.shape) != shape:
             raise ValueError(f"pools must be {shape}")
+        self.rope = rope
+        self.bounds = torch.zeros((num_blocks, num_kv_heads, 2, head_dim), dtype=self.k_pool.dtype,
+                                  device=self.device) if key_bounds else None
         self.alloc = B.Allocator(num_blocks, block_size, free_order)
         self._meta_cap = 0
         self._ws = None
@@ -68,8 +96,8 @@ class PagedKVCache:
 
     # -- metadata staging ----------------------------------------------------
     def _ensure_meta(self, n: int) -> None:
-        # layout (int32): slots[n] | seq_lens[n] | cow[2n] | tables[n * max_blocks]
-        need = n * (4 + self.max_blocks)
+        # layout (int32): slots[n] | seq_lens[n] | cow[2n] | tables[n * max_blocks] | positions[n]
+        need = n * (5 + self.max_blocks)
         if need <= self._meta_cap:
             return
         self._meta_host = torch.empty(need, dtype=torch.int32, pin_memory=True)
@@ -96,11 +124,14 @@ class PagedKVCache:
         i32p = lambda a: a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))  # noqa: E731
         check(lib().pkv_seq_append_slots(self.alloc._h, ip, n, i32p(slots), i32p(cow), n, ctypes.byref(ncow)))
         check(lib().pkv_block_tables(self.alloc._h, ip, n, self.max_blocks, i32p(tables), i32p(lens)))
+        if self.rope is not None:
+            at = n * (4 + self.max_blocks)
+            np.subtract(lens, 1, out=m[at:at + n])
         return ncow.value, (slots, lens, cow, tables)
 
     def upload_step(self, n: int):
         """Copy the staged metadata to the device; returns device views."""
-        used = n * (4 + self.max_blocks)
+        used = n * ((5 if self.rope is not None else 4) + self.max_blocks)
         self._meta_dev[:used].copy_(self._meta_host[:used], non_blocking=True)
         ev = torch.cuda.Event()
         ev.record()
@@ -120,19 +151,41 @@ class PagedKVCache:
 
     # -- the decode step -----------------------------------------------------
     def decode_step(self, seq_ids: Sequence[int], q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
-                    scale: float, partition_tokens: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    scale: float, partition_tokens: int = 0, out: Optional[torch.Tensor] = None,
+                    max_selected: Optional[int] = None, n_first: int = 1, n_last: int = 2) -> torch.Tensor:
         """Append one token per sequence and attend over every cached token.
 
         ``q`` [n, Hq, D], ``k_new``/``v_new`` [n, Hkv, D] in the pool dtype, on
         the device or in (pinned) host memory.  Returns float32 [n, Hq, D] on
         the device: ``out`` if given (a contiguous device tensor), else a
-        buffer of this cache valid until the next step."""
+        buffer of this cache valid until the next step.
+
+        With ``max_selected`` (a cache with ``key_bounds``) each sequence and
+        KV head attends over that many blocks at most: the first ``n_first``,
+        the last ``n_last`` and the best-scored of the others."""
+        if max_selected is not None and self.bounds is None:
+            raise ValueError("max_selected needs a cache made with key_bounds=True")
         n = len(seq_ids)
         ncow, _ = self.prepare_step(seq_ids)
         slots, lens, cow, tables = self.upload_step(n)
         q, k_new, v_new = (t.to(self.device, non_blocking=True) for t in (q, k_new, v_new))
         if ncow:
             B.pkv_copy_blocks(self.k_pool, self.v_pool, cow[:2 * ncow].view(ncow, 2))
+        if self.rope is not None or self.bounds is not None:
+            at = n * (4 + self.max_blocks)
+            q = self._append(q, k_new, v_new, slots, self._meta_dev[at:at + n])
+            if self.bounds is not None:
+                LC.pkv_block_bounds(self.k_pool, tables, lens, self.bounds)
+            if max_selected is not None:
+                return self._attend_selected(q, tables, lens, scale, max_selected, n_first, n_last, out)
+            ws, own = self._buffers(n, q.shape[1], partition_tokens)
+            out = own if out is None else out
+            if self.fp8:
+                return B.pkv_paged_attention_decode_fp8(q, self.k_pool, self.v_pool, tables, lens, scale, self.k_scale,
+                                                        self.v_scale, out=out, workspace=ws,
+                                                        partition_tokens=partition_tokens)
+            return B.pkv_paged_attention_decode(q, self.k_pool, self.v_pool, tables, lens, scale, out=out,
+                                                workspace=ws, partition_tokens=partition_tokens)
         ws, own = self._buffers(n, q.shape[1], partition_tokens)
         out = own if out is None else out
         if self.fp8:
@@ -141,6 +194,71 @@ class PagedKVCache:
                                                partition_tokens=partition_tokens)
         return B.pkv_append_and_decode(k_new, v_new, slots, q, self.k_pool, self.v_pool, tables, lens, scale,
                                        out=out, workspace=ws, partition_tokens=partition_tokens)
+
+    def _append(self, q, k_new, v_new, slots, positions) -> torch.Tensor:
+        """K and V into their slots, rotated if the cache rotates; returns q as
+        the attention takes it."""
+        if self.rope is None:
+            if self.fp8:
+                B.pkv_kv_append_fp8(k_new, v_new, slots, self.k_pool, self.v_pool, self.k_scale, self.v_scale)
+            else:
+                B.pkv_kv_append(k_new, v_new, slots, self.k_pool, self.v_pool)
+            return q
+        r = self.rope
+        args = (q, k_new, v_new, positions, r.inv_freq, slots, self.k_pool, self.v_pool)
+        if self.fp8:
+            return LC.pkv_rope_append_fp8(*args, self.k_scale, self.v_scale, r.interleaved, r.factor)
+        return LC.pkv_rope_append(*args, r.interleaved, r.factor)
+
+    def _attend_selected(self, q, tables, lens, scale, max_selected, n_first, n_last, out):
+        sel = LC.pkv_block_select(q, self.bounds, tables, lens, max_selected, self.block_size, n_first, n_last)
+        if out is None:
+            shape = tuple(q.shape)
+            if self._out is None or tuple(self._out.shape) != shape:
+                self._out = torch.empty(shape, dtype=torch.float32, device=self.device)
+            out = self._out
+        if self.fp8:
+            return LC.pkv_paged_attention_decode_sparse_fp8(q, self.k_pool, self.v_pool, tables, lens, sel, scale,
+                                                            self.k_scale, self.v_scale, out=out)
+        return LC.pkv_paged_attention_decode_sparse(q, self.k_pool, self.v_pool, tables, lens, sel, scale, out=out)
+
+    # -- prompts -------------------------------------------------------------
+    def write_chunk(self, seq_ids: Sequence[int], n_new: Sequence[int], q: torch.Tensor, k_new: torch.Tensor,
+                    v_new: torch.Tensor):
+        """Write the K/V rows of the last ``n_new[i]`` tokens of each sequence
+        (admitted with :meth:`add` or :meth:`add_cached`; their blocks not
+        shared with another sequence), row by row in sequence order, and
+        refresh the key bounds.  ``q`` [sum(n_new), Hq, D], ``k_new`` /
+        ``v_new`` [sum(n_new), Hkv, D] on the device.  Returns what
+        pkv_paged_attention_prefill takes: q (rotated if the cache rotates),
+        block tables, lengths and q_start."""
+        n_new = np.asarray(n_new, dtype=np.int64)
+        tables, lens = self.alloc.block_tables(seq_ids, self.max_blocks)
+        if n_new.shape != lens.shape or (n_new < 0).any() or (n_new > lens).any():
+            raise ValueError("n_new must hold, for each sequence, a count of at most its length")
+        start = np.zeros(len(lens) + 1, dtype=np.int64)
+        np.cumsum(n_new, out=start[1:])
+        if start[-1] != k_new.shape[0]:
+            raise ValueError(f"n_new sums to {start[-1]}, k_new has {k_new.shape[0]} rows")
+        seq = np.repeat(np.arange(len(lens)), n_new)
+        pos = np.arange(start[-1]) - start[seq] + (lens - n_new)[seq]
+        slots = tables[seq, pos // self.block_size].astype(np.int64) * self.block_size + pos % self.block_size
+        up = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(self.device)  # noqa: E731
+        tables, lens, new = up(tables), up(lens), up(n_new)
+        q = self._append(q, k_new, v_new, up(slots), up(pos))
+        if self.bounds is not None and start[-1]:
+            LC.pkv_block_bounds(self.k_pool, tables, lens, self.bounds, new, int(n_new.max()))
+        return q, tables, lens, up(start)
+
+    def refresh_bounds(self, seq_ids: Sequence[int]) -> None:
+        """Recompute the key bounds of every block of these sequences (rows
+        written into the pool by other means)."""
+        if self.bounds is None:
+            raise ValueError("the cache was made without key_bounds")
+        tables, lens = self.alloc.block_tables(seq_ids, self.max_blocks)
+        if lens.size and lens.max() > 0:
+            t, n = torch.from_numpy(tables).to(self.device), torch.from_numpy(lens).to(self.device)
+            LC.pkv_block_bounds(self.k_pool, t, n, self.bounds, n, int(lens.max()))
 
     # -- the decode step in one library call -------------------------------
     def decode_step_host(self, seq_ids: np.ndarray, q_host: torch.Tensor, k_host: torch.Tensor,
@@ -159,6 +277,8 @@ class PagedKVCache:
         they proceed under the neighbouring steps' kernels (two sets of device
         buffers alternate); ``out_host`` is then complete once the current
         stream and the copy streams have been synchronised."""
+        if self.rope is not None or self.bounds is not None:
+            raise ValueError("decode_step_host neither rotates nor keeps key bounds: use decode_step")
         ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
         n = int(ids.size)
         hq = q_host.shape[1]
