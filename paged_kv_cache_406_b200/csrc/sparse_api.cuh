@@ -106,18 +106,24 @@ SparseLayout sparse_layout(int64_t rows, int32_t group, int32_t head_dim, int32_
   return w;
 }
 
-template <typename T, int D, int G>
-int launch_sparse(const pkv::SparseDecodeArgs& a, const char* fn, cudaStream_t s) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  const int64_t rows = int64_t(a.s.num_seqs) * a.s.num_kv_heads;
-  const int64_t chunks = (int64_t(a.s.max_selected) * a.s.block_size + 15) / 16;
-  int ctas = 1;  // as many as are resident at once (two an SM) and have a chunk for each warp
-  while (ctas < pkv::kSparseCluster && rows * ctas <= sm_count(dev) && chunks >= 2 * ctas * pkv::kSparseWarps) ctas *= 2;
+template <typename T, int D, int G, int kWarps>
+int launch_sparse(const pkv::SparseDecodeArgs& a, int ctas, int dev, const CUtensorMap& mk, const CUtensorMap& mv,
+                  const char* fn, cudaStream_t s) {
+  auto kern = pkv::sparse_decode_kernel<T, D, G, kWarps>;
+  constexpr int kSmem = pkv::SparseSmem<T, D, G, kWarps>::kBytes;
+  static std::atomic<bool> opted[kMaxDevices];
+  cudaError_t e;
+  if (dev >= kMaxDevices || !opted[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sparse)");
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(carveout)");
+    if (dev < kMaxDevices) opted[dev].store(true, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
-  cfg.blockDim = dim3(pkv::kSparseThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.s.num_seqs) * a.s.num_kv_heads * ctas));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -127,18 +133,44 @@ int launch_sparse(const pkv::SparseDecodeArgs& a, const char* fn, cudaStream_t s
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, pkv::sparse_decode_kernel<T, D, G>, a);
+  e = cudaLaunchKernelEx(&cfg, kern, a, mk, mv);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return pkv::ok();
 }
 
+template <typename T, int D, int G>
+int launch_sparse_shape(const pkv::SparseDecodeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, const char* fn,
+                        cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int64_t rows = int64_t(a.s.num_seqs) * a.s.num_kv_heads, sms = sm_count(dev);
+  const int64_t chunks = (int64_t(a.s.max_selected) * a.s.block_size + 15) / 16;
+  // CTAs of a row: as many as leave each warp a chunk and are resident at once
+  auto spread = [&](int warps, int64_t slots) {
+    int ctas = 1;
+    while (ctas < pkv::kSparseCluster && rows * ctas * 2 <= slots && chunks >= 2 * ctas * warps) ctas *= 2;
+    return ctas;
+  };
+  if (rows <= sms) return launch_sparse<T, D, G, pkv::kSparseManyWarps>(a, spread(pkv::kSparseManyWarps, sms), dev, mk, mv, fn, s);
+  return launch_sparse<T, D, G, pkv::kSparseFewWarps>(a, spread(pkv::kSparseFewWarps, 4 * sms), dev, mk, mv, fn, s);
+}
+
 template <typename T, int D>
-int launch_sparse_group(const pkv::SparseDecodeArgs& a, int32_t group, const char* fn, cudaStream_t s) {
+int launch_sparse_group(const pkv::SparseDecodeArgs& a, const void* k_pool, const void* v_pool, int dtype, int32_t group,
+                        const char* fn, cudaStream_t s) {
+  const int64_t rows = int64_t(a.s.num_blocks) * a.s.num_kv_heads * a.s.block_size;
+  const int box_rows = a.s.block_size < 16 ? a.s.block_size : 16;
+  CUtensorMap mk, mv;
+  int rc = pool_map(&mk, k_pool, dtype, rows, D, box_rows);
+  if (rc) return rc;
+  rc = pool_map(&mv, v_pool, dtype, rows, D, box_rows);
+  if (rc) return rc;
   switch (group) {
-    case 1: return launch_sparse<T, D, 1>(a, fn, s);
-    case 2: return launch_sparse<T, D, 2>(a, fn, s);
-    case 4: return launch_sparse<T, D, 4>(a, fn, s);
-    default: return launch_sparse<T, D, 8>(a, fn, s);
+    case 1: return launch_sparse_shape<T, D, 1>(a, mk, mv, fn, s);
+    case 2: return launch_sparse_shape<T, D, 2>(a, mk, mv, fn, s);
+    case 4: return launch_sparse_shape<T, D, 4>(a, mk, mv, fn, s);
+    default: return launch_sparse_shape<T, D, 8>(a, mk, mv, fn, s);
   }
 }
 
@@ -174,17 +206,18 @@ int sparse_decode(const char* fn, const void* q, const void* k_pool, const void*
                           num_blocks, block_size};
   if (sparse_by_cluster(dtype, max_selected)) {
     const double k = dtype == PKV_FP8_E4M3 ? k_scale : 1.0;
-    const pkv::SparseDecodeArgs d{a, q, k_pool, v_pool, out,
-                                  static_cast<float>(static_cast<double>(scale) * k * 1.4426950408889634), v_scale};
+    const pkv::SparseDecodeArgs d{a, q, out, static_cast<float>(static_cast<double>(scale) * k * 1.4426950408889634),
+                                  v_scale};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool d128 = head_dim == 128;
     switch (dtype) {
       case PKV_BF16:
-        return d128 ? launch_sparse_group<__nv_bfloat16, 128>(d, group, fn, s)
-                    : launch_sparse_group<__nv_bfloat16, 64>(d, group, fn, s);
+        return d128 ? launch_sparse_group<__nv_bfloat16, 128>(d, k_pool, v_pool, dtype, group, fn, s)
+                    : launch_sparse_group<__nv_bfloat16, 64>(d, k_pool, v_pool, dtype, group, fn, s);
       case PKV_F16:
-        return d128 ? launch_sparse_group<__half, 128>(d, group, fn, s) : launch_sparse_group<__half, 64>(d, group, fn, s);
-      default: return launch_sparse_group<pkv::E4m3, 128>(d, group, fn, s);
+        return d128 ? launch_sparse_group<__half, 128>(d, k_pool, v_pool, dtype, group, fn, s)
+                    : launch_sparse_group<__half, 64>(d, k_pool, v_pool, dtype, group, fn, s);
+      default: return launch_sparse_group<pkv::E4m3, 128>(d, k_pool, v_pool, dtype, group, fn, s);
     }
   }
   if (!workspace) return fail(PKV_ERR_INVALID_ARG, "%s: NULL pointer", fn);

@@ -3,6 +3,8 @@
 // selected[b][g][...] (ascending logical indices, -1 after the last) only.
 #pragma once
 
+#include <cuda.h>
+
 #include "block_select.cuh"
 #include "decode.cuh"
 #include "device_common.cuh"
@@ -72,45 +74,64 @@ __global__ void __launch_bounds__(256) expand_selection_kernel(const SparseArgs 
 // 16-token chunks in turn, each with its own online softmax, and the cluster
 // joins them through distributed shared memory.
 //
-// A warp holds a chunk in registers, loaded from the pool as it is used:
+// A warp streams its chunks through 16 KB of shared memory of its own (tensor
+// map loads issued by its lane 0, 128-byte swizzle), so it waits for nothing
+// but its own next chunk:
 //     S[8 heads][16 tokens]   = Q[8 (of 16)][D] . K^T        (two 8-token tiles)
 //     O^T[D][8 heads]        += V^T[D][16 tokens] . P^T[16][8]
-// Lane (q, t) = (lane / 4, lane % 4) loads 16-byte pieces of K rows q and
+// Lane (q, t) = (lane / 4, lane % 4) reads 16-byte pieces of K rows q and
 // q + 8, which are B fragments of S in a channel order that Q's fragments
 // share, and of V rows 2t, 2t + 1, 2t + 8, 2t + 9, whose halves exchanged
 // (prmt) are A fragments of O^T in an order of channels undone at the end.
 // S leaves each lane with head q at tokens 2t, 2t + 1, 2t + 8, 2t + 9: P's B
-// fragments as they are.  The next chunk's K is loaded when S is done, its V
-// when O is.  P enters as a sum of two f16 or three bf16 values (22 or 24
-// bits), so its rounding does not show in a 32-bit result.
+// fragments as they are.  P enters as a sum of two f16 or three bf16 values
+// (22 or 24 bits), so its rounding does not show in a 32-bit result.
 // ---------------------------------------------------------------------------
-constexpr int kSparseWarps = 8;
-constexpr int kSparseThreads = kSparseWarps * 32;
-constexpr int kSparseList = 1024;   // most selected blocks (their tiles lie in shared memory)
+constexpr int kSparseList = 1024;   // most selected blocks (they lie in shared memory)
 constexpr int kSparseCluster = 8;
+// Warps of a CTA: three where there are many rows (four CTAs an SM, so that 592
+// rows run at once and end together), eight where there are few.
+constexpr int kSparseFewWarps = 3, kSparseManyWarps = 8;
+
+template <typename T, int D, int G, int kWarps>
+struct SparseSmem {
+  static constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes of a token
+  static constexpr int kTile = 16 * kRow;                       // K (or V) of a chunk
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = 16 * 1024 / kStage;            // 2 or 4
+  static constexpr int kRec = (G * D + 2 * G + 3) / 4 * 4;      // O, m, l of a warp or a CTA; 16-byte aligned
+  static constexpr int kRing = kWarps * kStages * kStage;       // the records take its place at the end
+  static constexpr int kRecBytes = kWarps * kRec * 4;
+  static constexpr int kBytes = 1024 + (kRing > kRecBytes ? kRing : kRecBytes);  // 1024: the swizzle's alignment
+};
 
 struct SparseDecodeArgs {
   SparseArgs s;
   const void* q;
-  const void* k_pool;
-  const void* v_pool;
   float* out;
   float scale_log2, v_scale;
 };
 
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const SparseDecodeArgs a) {
+template <typename T, int D, int G, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1)
+    sparse_decode_kernel(const SparseDecodeArgs a, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap) {
   using Q = typename QueryOf<T>::type;
+  using Smem = SparseSmem<T, D, G, kWarps>;
   constexpr bool kFp8 = sizeof(T) == 1;
-  constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes
+  constexpr int kThreads = kWarps * 32, kRow = Smem::kRow, kNS = Smem::kStages, kRec = Smem::kRec;
   constexpr int kKP = kRow / 64, kVP = kRow / 128;       // pieces of a K row (four lanes) and a V row (eight lanes)
   constexpr int kSteps = kFp8 ? 4 : 2;                   // mma steps of a K piece
   constexpr int kTiles = kFp8 ? 8 : 4;                   // channel pairs of a V piece
   constexpr int kTerms = std::is_same_v<Q, __nv_bfloat16> ? 3 : 2;
-  constexpr int kRec = (G * D + 2 * G + 3) / 4 * 4;      // O, m, l of a warp or a CTA; 16-byte aligned
+  extern __shared__ unsigned char sparse_raw[];
   __shared__ int32_t list[kSparseList];
   __shared__ int32_t first_bad;
-  __shared__ __align__(16) float rec[kSparseWarps][kRec];
+  __shared__ int32_t abort_word;
+  __shared__ __align__(8) uint64_t full[kWarps][kNS];
+  unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sparse_raw) + 1023) & ~uintptr_t(1023));
+  float* rec = reinterpret_cast<float*>(ring);  // [kWarps][kRec], once the ring is done with
+  volatile int* abort_flag = &abort_word;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint32_t rank, ctas;
@@ -128,7 +149,13 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
   const int nblk = fits ? (L + bs - 1) >> bs_shift : 0;
   if (tid == 0) {
     first_bad = K;
+    abort_word = 0;
     if (!fits && rank == 0) record_error(PKV_ERR_INVALID_ARG);
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kNS; ++i) mbar_init(smem_addr(&full[w][i]), 1);
+    fence_mbar_init();
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
   }
   // A fragments of Q: row gq is head gq (zero from G on, as are rows 8 .. 15)
   uint32_t qa[kKP][kSteps][2];
@@ -143,7 +170,7 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
       qa[i][s][1] = w.y;
     }
   __syncthreads();
-  for (int i = tid; i < K; i += kSparseThreads) {
+  for (int i = tid; i < K; i += kThreads) {
     const int j = sel[i], before = i ? sel[i - 1] : -1;
     if (j >= 0 && j < nblk && j > before) {
       int phys = a.s.block_tables[static_cast<int64_t>(b) * a.s.max_blocks + j];
@@ -158,7 +185,7 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
   __syncthreads();
   const int n = first_bad;  // the list's length
   if (rank == 0 && tid == 0 && n < K && sel[n] >= 0 && fits) record_error(PKV_ERR_INVALID_ARG);
-  for (int i = tid; i < n; i += kSparseThreads) {
+  for (int i = tid; i < n; i += kThreads) {
     if (list[i] < 0) {
       record_error(PKV_ERR_BAD_BLOCK);
       list[i] = 0;
@@ -168,33 +195,35 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
   const int tokens = n ? ((n - 1) << bs_shift) + min(bs, L - (sel[n - 1] << bs_shift)) : 0;
   const int chunks = (tokens + 15) >> 4;
 
-  const unsigned char* kbase = static_cast<const unsigned char*>(a.k_pool) + (g << bs_shift) * static_cast<int64_t>(kRow);
-  const unsigned char* vbase = static_cast<const unsigned char*>(a.v_pool) + (g << bs_shift) * static_cast<int64_t>(kRow);
-  const int64_t tile_bytes = static_cast<int64_t>(a.s.num_kv_heads) * bs * kRow;
-  auto row_at = [&](int token) {  // byte offset of a token's row
-    return list[token >> bs_shift] * tile_bytes + (token & (bs - 1)) * kRow;
-  };
-  uint4 kx[2][kKP], vx[4][kVP];
-  auto load_k = [&](int c) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int token = c * 16 + gq + 8 * r;
-      const bool live = token < tokens;
-      const uint4* src = reinterpret_cast<const uint4*>(kbase + row_at(live ? token : 0)) + tq;
-#pragma unroll
-      for (int i = 0; i < kKP; ++i) kx[r][i] = live ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
+  // ---- the warp's ring ----
+  // A tile lies as the tensor map's boxes of `box` rows: [box][128-byte half][row]
+  // [128 B], 16-byte pieces exchanged by the row's number mod 8.
+  const int box = min(bs, 16), step = static_cast<int>(ctas) * kWarps, c_first = static_cast<int>(rank) * kWarps + warp;
+  const uint32_t ring_s = smem_addr(ring) + warp * kNS * Smem::kStage;
+  const uint64_t policy = l2_evict_first_policy();
+  auto issue = [&](int c, int stage) {  // lane 0
+    const uint32_t bar = smem_addr(&full[warp][stage]), dst = ring_s + stage * Smem::kStage;
+    const int boxes = bs == 8 ? min(2, n - 2 * c) : 1;
+    mbar_arrive_expect_tx(bar, boxes * 2 * box * kRow);
+    for (int i = 0; i < boxes; ++i) {
+      const int token = c * 16 + i * 8;
+      const int y = (list[token >> bs_shift] * a.s.num_kv_heads + g) * bs + (token & (bs - 1));
+      tma_load_3d(dst + i * box * kRow, &kmap, 0, y, 0, bar, policy);
+      tma_load_3d(dst + Smem::kTile + i * box * kRow, &vmap, 0, y, 0, bar, policy);
     }
   };
-  auto load_v = [&](int c) {  // rows behind the last token are zero: whatever lies there is not read
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int token = c * 16 + 2 * tq + (r & 1) + 8 * (r >> 1);
-      const bool live = token < tokens;
-      const uint4* src = reinterpret_cast<const uint4*>(vbase + row_at(live ? token : 0)) + gq;
-#pragma unroll
-      for (int i = 0; i < kVP; ++i) vx[r][i] = live ? __ldg(src + 8 * i) : make_uint4(0, 0, 0, 0);
-    }
+  // 16 bytes at byte `at` of row r of a tile
+  auto piece = [&](uint32_t tile, int r, int at) {
+    const int rr = r & (box - 1);
+    const uint32_t addr = tile + (r - rr) * kRow + ((at >> 7) * box + rr) * 128 + ((((at >> 4) & 7) ^ (rr & 7)) << 4);
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
   };
+  if (lane == 0) {
+    for (int i = 0; i < kNS; ++i)
+      if (c_first + i * step < chunks) issue(c_first + i * step, i);
+  }
 
   float acc[kVP][kTiles][4];
 #pragma unroll
@@ -202,20 +231,30 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
   float m = -INFINITY, l = 0.f;  // of head gq
-  const int step = static_cast<int>(ctas) * kSparseWarps;
-  int c = static_cast<int>(rank) * kSparseWarps + warp;
-  if (c < chunks) {
-    load_k(c);
-    load_v(c);
-  }
-  for (; c < chunks; c += step) {
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int c = c_first; c < chunks; c += step) {
+    const bool landed = __all_sync(kFull, mbar_wait(smem_addr(&full[warp][stage]), phase, abort_flag));
+    if (!landed) {  // give up, after the copies that are still on their way
+      if (lane == 0) {
+        record_error(PKV_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+        for (int i = 0; i < kNS && c + i * step < chunks; ++i) {
+          const int st = (stage + i) % kNS;
+          mbar_drain(smem_addr(&full[warp][st]), st < stage ? phase ^ 1 : phase);
+        }
+      }
+      break;
+    }
+    const uint32_t ktile = ring_s + stage * Smem::kStage, vtile = ktile + Smem::kTile;
     // ---- scores ----
     float s[2][4] = {};
 #pragma unroll
     for (int i = 0; i < kKP; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint32_t v[4] = {kx[r][i].x, kx[r][i].y, kx[r][i].z, kx[r][i].w};
+        const uint4 x = piece(ktile, gq + 8 * r, i * 64 + tq * 16);
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int t = 0; t < kSteps; ++t) {
           const uint32_t qf[4] = {qa[i][t][0], 0u, qa[i][t][1], 0u};
@@ -224,7 +263,6 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
         }
       }
     const int nv = tokens - c * 16;  // valid tokens from the chunk's first
-    if (c + step < chunks) load_k(c + step);
     float x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -271,7 +309,10 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
       uint32_t w[4][kTiles];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t v[4] = {vx[r][i].x, vx[r][i].y, vx[r][i].z, vx[r][i].w};
+        const int token = 2 * tq + (r & 1) + 8 * (r >> 1);
+        uint4 y = piece(vtile, token, i * 128 + gq * 16);
+        if (token >= nv) y = make_uint4(0, 0, 0, 0);  // whatever lies behind the last token
+        const uint32_t v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if constexpr (kFp8) {
@@ -291,13 +332,19 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
         for (int k = 0; k < kTerms; ++k) mma_16816<Q>(acc[i][t], f, pb[k][0], pb[k][1]);
       }
     }
-    if (c + step < chunks) load_v(c + step);
+    __syncwarp();  // every lane has read the stage
+    if (lane == 0 && c + kNS * step < chunks) issue(c + kNS * step, stage);
+    if (++stage == kNS) {
+      stage = 0;
+      phase ^= 1;
+    }
   }
 
   // ---- join the warps ----
   l += __shfl_xor_sync(kFull, l, 1);
   l += __shfl_xor_sync(kFull, l, 2);
-  float* mine = rec[warp];
+  __syncthreads();  // the ring's place is free
+  float* mine = rec + warp * kRec;
 #pragma unroll
   for (int i = 0; i < kVP; ++i)
 #pragma unroll
@@ -314,38 +361,38 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
   }
   __syncthreads();
   // the CTA's record takes the place of warp 0's: each thread rewrites only what it alone reads
-  float mh[kSparseWarps];
+  float mh[kWarps];
   auto factors = [&](int h) {
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) top = fmaxf(top, rec[w][G * D + h]);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, rec[w * kRec + G * D + h]);
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) mh[w] = top == -INFINITY ? 0.f : fast_exp2(rec[w][G * D + h] - top);
+    for (int w = 0; w < kWarps; ++w) mh[w] = top == -INFINITY ? 0.f : fast_exp2(rec[w * kRec + G * D + h] - top);
     return top;
   };
-  for (int e = tid * 4; e < G * D; e += kSparseThreads * 4) {
+  for (int e = tid * 4; e < G * D; e += kThreads * 4) {
     factors(e / D);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(&rec[w][e]);
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(&rec[w * kRec + e]);
       o.x += mh[w] * y.x;
       o.y += mh[w] * y.y;
       o.z += mh[w] * y.z;
       o.w += mh[w] * y.w;
     }
-    *reinterpret_cast<float4*>(&rec[0][e]) = o;
+    *reinterpret_cast<float4*>(&rec[e]) = o;
   }
   float cta_m = 0.f, cta_l = 0.f;
   if (tid < G) {
     cta_m = factors(tid);
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) cta_l += mh[w] * rec[w][G * D + G + tid];
+    for (int w = 0; w < kWarps; ++w) cta_l += mh[w] * rec[w * kRec + G * D + G + tid];
   }
   __syncthreads();
   if (tid < G) {
-    rec[0][G * D + tid] = cta_m;
-    rec[0][G * D + G + tid] = cta_l;
+    rec[G * D + tid] = cta_m;
+    rec[G * D + G + tid] = cta_l;
   }
 
   // ---- join the CTAs: each finishes a share of the outputs ----
@@ -356,14 +403,14 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(p)), "r"(r));
     return addr;
   };
-  for (int e = (static_cast<int>(rank) * kSparseThreads + tid) * 4; e < G * D; e += static_cast<int>(ctas) * kSparseThreads * 4) {
+  for (int e = (static_cast<int>(rank) * kThreads + tid) * 4; e < G * D; e += static_cast<int>(ctas) * kThreads * 4) {
     const int h = e / D;
     float cm[kSparseCluster], top = -INFINITY, den = 0.f;
 #pragma unroll
     for (int r = 0; r < kSparseCluster; ++r) {
       cm[r] = -INFINITY;
       if (r < static_cast<int>(ctas))
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(cm[r]) : "r"(remote(&rec[0][G * D + h], r)) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(cm[r]) : "r"(remote(&rec[G * D + h], r)) : "memory");
       top = fmaxf(top, cm[r]);
     }
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -372,10 +419,10 @@ __global__ void __launch_bounds__(kSparseThreads, 2) sparse_decode_kernel(const 
       if (r < static_cast<int>(ctas)) {
         float cl;
         float4 y;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(cl) : "r"(remote(&rec[0][G * D + G + h], r)) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(cl) : "r"(remote(&rec[G * D + G + h], r)) : "memory");
         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                     : "r"(remote(&rec[0][e], r))
+                     : "r"(remote(&rec[e], r))
                      : "memory");
         const float f = top == -INFINITY ? 0.f : fast_exp2(cm[r] - top);
         den += f * cl;
