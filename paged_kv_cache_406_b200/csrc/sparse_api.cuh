@@ -146,10 +146,15 @@ int launch_sparse_shape(const pkv::SparseDecodeArgs& a, const CUtensorMap& mk, c
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   const int64_t rows = int64_t(a.s.num_seqs) * a.s.num_kv_heads, sms = sm_count(dev);
   const int64_t chunks = (int64_t(a.s.max_selected) * a.s.block_size + 15) / 16;
-  // CTAs of a row: as many as leave each warp a chunk and are resident at once
+  // CTAs of a row: as many as leave each warp a chunk and are resident at
+  // once.  Eight-warp CTAs fill an SM, and clusters of eight do not pack the
+  // SMs of a GPU partition: 16 rows of 256 blocks took 20 us in 16 clusters of
+  // eight and 13.3 in clusters of four, 8 rows of 64 blocks 7.0 in clusters of
+  // eight and 7.1 of four; 32 rows 8.6 in clusters of four and 9.2 of two.
   auto spread = [&](int warps, int64_t slots) {
     int ctas = 1;
-    while (ctas < pkv::kSparseCluster && rows * ctas * 2 <= slots && chunks >= 2 * ctas * warps) ctas *= 2;
+    while (ctas < pkv::kSparseCluster && rows * ctas * 2 <= (ctas * 2 == 8 ? slots / 2 : slots) && chunks >= 2 * ctas * warps)
+      ctas *= 2;
     return ctas;
   };
   if (rows <= sms) return launch_sparse<T, D, G, pkv::kSparseManyWarps>(a, spread(pkv::kSparseManyWarps, sms), dev, mk, mv, fn, s);
