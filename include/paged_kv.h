@@ -546,7 +546,7 @@ int pkv_rope(const void* x, int64_t x_stride, const int32_t* positions, const do
  * the three may be views of one projection's output.  Slots as for
  * pkv_kv_append (slot < 0: q is rotated, nothing is written to the pools).
  * num_q_heads = 0 leaves q and q_out out.  head_dim 64 or 128, block_size 8,
- * 16 or 32.  q_out must not overlap q. */
+ * 16 or 32.  q_out must not overlap q, k or v. */
 int pkv_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                     int64_t v_stride, const int32_t* positions, const double* inv_freq, const int32_t* slot_mapping,
                     int32_t n_tokens, void* q_out, void* k_pool, void* v_pool, int32_t num_blocks,
@@ -576,7 +576,8 @@ int pkv_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t 
  * new_tokens[b] tokens of sequence b (int32[num_seqs] on the device, at most
  * max_new_tokens each; NULL: one token each, a decode step, none for an empty
  * sequence), over all of the block's tokens below seq_lens[b]; no others.
- * Call it after the append.  NaN keys give NaN bounds.  A sequence whose
+ * Call it after the append.  A block that two sequences of the call list at
+ * different fills takes the bounds of either.  NaN keys give NaN bounds.  A sequence whose
  * length is outside its table or whose new_tokens is negative, above
  * max_new_tokens or above its length is skipped and recorded as
  * PKV_ERR_INVALID_ARG, a block id outside the pool as PKV_ERR_BAD_BLOCK (that
@@ -623,7 +624,8 @@ int pkv_sparse_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num
  * [max_selected], logical indices, strictly ascending, -1 behind the last).
  * A list ends at its first negative entry, and at one that is not above its
  * predecessor or lies beyond the sequence, which is recorded as
- * PKV_ERR_INVALID_ARG.  An empty list gives zeros.  A length outside the
+ * PKV_ERR_INVALID_ARG.  An empty list gives zeros.  Rows behind the last
+ * token of a sequence are not used, whatever they hold.  A length outside the
  * table is recorded as PKV_ERR_INVALID_ARG and gives zeros, a block id outside
  * the pool as PKV_ERR_BAD_BLOCK (block 0 is read instead).  fp32 pools: up to
  * 4 query heads per KV head.  workspace: at least

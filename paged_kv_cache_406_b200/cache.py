@@ -70,6 +70,9 @@ class PagedKVCache:
         self.v_pool = v_pool if v_pool is not None else torch.empty(shape, dtype=dtype, device=self.device)
         if tuple(self.k_pool.shape) != shape or tuple(self.v_pool.shape) != shape:
             raise ValueError(f"pools must be {shape}")
+        if rope is not None and (rope.inv_freq.dtype != torch.float64 or 2 * rope.inv_freq.numel() > head_dim
+                                 or rope.inv_freq.get_device() != self.k_pool.get_device()):
+            raise ValueError("rope.inv_freq must be float64, on the cache's device, at most head_dim / 2 long")
         self.rope = rope
         self.bounds = torch.zeros((num_blocks, num_kv_heads, 2, head_dim), dtype=self.k_pool.dtype,
                                   device=self.device) if key_bounds else None
@@ -165,6 +168,8 @@ class PagedKVCache:
         the last ``n_last`` and the best-scored of the others."""
         if max_selected is not None and self.bounds is None:
             raise ValueError("max_selected needs a cache made with key_bounds=True")
+        if max_selected is not None and (n_first < 0 or n_last < 0 or max_selected < max(1, n_first + n_last)):
+            raise ValueError("n_first + n_last must be at most max_selected, which must be positive")
         n = len(seq_ids)
         ncow, _ = self.prepare_step(seq_ids)
         slots, lens, cow, tables = self.upload_step(n)

@@ -30,7 +30,9 @@ struct E4m3 {
 // bounds: one warp per (sequence, touched block, KV head).  Bytes bound it:
 // every row of a touched block is read once.  A row is D * sizeof(T) / 16
 // lanes wide; the warp's lane groups take the rows in turn, each lane keeps
-// the minimum and maximum of its 16 bytes, and the groups join by shuffles.
+// the minimum and maximum of its 16 bytes, and the groups join by shuffles.  16
+// prompts of up to 4096 f16 tokens (107 MB): 19 us, 5.6 TB/s; one block for
+// each of 64 sequences: 2.3 us.
 // ---------------------------------------------------------------------------
 struct BoundsArgs {
   const void* k_pool;
@@ -198,7 +200,10 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 
 // ---------------------------------------------------------------------------
 // selection: score_kernel, then select_kernel with one CTA per (sequence, KV
-// head).
+// head): 256 threads and four CTAs an SM, or 1024 threads for few long rows (16
+// rows of 8192 blocks: 24.5 us in all against 31; 512 rows of 2048: 71 against
+// 99).  The selection is a chain of short steps on one row (7 us for 512
+// blocks, 12 for 8192) and bound by their latency.
 // ---------------------------------------------------------------------------
 struct TileStats {  // of 16 scores
   uint32_t min_key, max_key;  // the candidates' keys
@@ -228,7 +233,8 @@ constexpr int kSelectFine = 512;    // border blocks ranked in shared memory
 // 32-bit sums of 2 D = 256 products lose at most 256 x 2^-24 = 2^-16 of that.
 // Tensor cores align the 16 products and the sum of a step to the largest of
 // them and drop bits below 2^-23 of it: 17 x 2^-23 a step, 16 steps, 2^-14.9.
-constexpr float kScoreError = 1.0f / 16384;
+// Products below 2^-126 may be lost altogether: 256 of them are below 1e-35.
+constexpr float kScoreError = 1.0f / 16384, kScoreTiny = 1e-35f;
 
 // Blocks of sequence b (0 for a length outside the table's capacity, which is
 // recorded).
@@ -451,7 +457,10 @@ struct Scorer<float, D, G> {
 // heads of the group.  The tiles of 16 blocks of all rows that have a choice
 // to make are numbered in order and dealt out to the warps of a resident grid
 // in equal runs, whatever the mix of lengths: a warp keeps q of its row in
-// registers and streams the row's tiles.
+// registers and streams the row's tiles.  64 contexts of 8K to 32K tokens (337
+// MB of bf16 bounds): 58 us, 5.8 TB/s.  A CTA or a cluster per row took 79 to
+// 97 us there (the longest row ends last); loads through shared memory
+// (cp.async) 78, for the instructions around them.
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
 
@@ -567,8 +576,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectArg
 }
 
 // The score of block j in 64 bits, as a key (in all lanes of the warp).  q:
-// the group's rows in 64 bits, in shared memory.
-template <typename T, int D, int G>
+// the group's rows in 64 bits, in shared memory.  kFinite: no infinity or NaN
+// is among the row's values, so the product with zero need not be formed.
+template <typename T, int D, int G, bool kFinite>
 __device__ __forceinline__ uint64_t fine_key(const SelectArgs& a, const double (&q)[G][D], int b, int g, int j) {
   constexpr int kPer = D / 32;  // a lane's channels, adjacent
   const int lane = threadIdx.x & 31, d0 = lane * kPer;
@@ -587,7 +597,9 @@ __device__ __forceinline__ uint64_t fine_key(const SelectArgs& a, const double (
 #pragma unroll
     for (int h = 0; h < G; ++h) {
       const double x = q[h][d0 + i];
-      s[h] += (x > 0 ? 0.0 : x) * lo + (x < 0 ? 0.0 : x) * hi;
+      const bool down = __double2hiint(x) < 0;  // by the sign bit: a comparison would cost as much as a product
+      if constexpr (kFinite) s[h] += x * (down ? lo : hi);
+      else s[h] += (down ? x : 0.0) * lo + (down ? 0.0 : x) * hi;
     }
   }
   // sums over the lanes: while there are heads to share out, a lane keeps
@@ -633,10 +645,7 @@ __device__ __forceinline__ int find_bin(const int* hist, int need, int* above, i
   }
   if (lane == 31) red[warp] = before;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w)
-    if (w < warp) before += red[w];
-  before -= mine;
+  before += __reduce_add_sync(kFull, lane < warp ? red[lane] : 0) - mine;
   if (before < need && before + mine >= need) {
     int run = before, bin = top;
 #pragma unroll
@@ -727,17 +736,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
     for (int i = tid; i < kSelectBins; i += kThreads) hist[i] = 0;
     if (tid < 2) count[tid] = 0;
     __syncthreads();
-    uint32_t base = 0xffffffffu, last = 0;
-    float big = 0.f, q1 = 0.f;
+    const TileStats st = warp_stats[lane % kWarps];
+    uint32_t base = __reduce_min_sync(kFull, st.min_key), last = __reduce_max_sync(kFull, st.max_key);
+    float big = st.big, q1 = q_norm[lane % G];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      base = min(base, warp_stats[w].min_key);
-      last = max(last, warp_stats[w].max_key);
-      big = MinMax<float>::mx(big, warp_stats[w].big);
+    for (int o = 16; o; o >>= 1) {
+      big = MinMax<float>::mx(big, __shfl_xor_sync(kFull, big, o));
+      q1 = MinMax<float>::mx(q1, __shfl_xor_sync(kFull, q1, o));
     }
-#pragma unroll
-    for (int h = 0; h < G; ++h) q1 = MinMax<float>::mx(q1, q_norm[h]);
-    const float eps = q1 * big * kScoreError;
+    const float eps = q1 * big * kScoreError + kScoreTiny;
     const bool bounded = eps <= 1e30f;  // false for infinities and NaN: every candidate is scored in 64 bits
 
     // ---- narrow the keys' range to a bin that holds the need0-th largest ----
@@ -798,7 +805,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
     if (n_near <= kSelectFine) {
       if (n_near > need) {
         for (int i = warp; i < n_near; i += kWarps) {
-          const uint64_t k = fine_key<T, D, G>(a, q_fine, b, g, fine_at[i]);
+          const int j = fine_at[i];
+          const uint64_t k =
+              bounded ? fine_key<T, D, G, true>(a, q_fine, b, g, j) : fine_key<T, D, G, false>(a, q_fine, b, g, j);
           if (lane == 0) fine[i] = k;
         }
         __syncthreads();
@@ -819,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
       for (int j = c0 + warp; j < c1; j += kWarps) {
         const float s = scores[j];
         if (bounded && (s > in_above || s < out_below)) continue;
-        const uint64_t k = fine_key<T, D, G>(a, q_fine, b, g, j);
+        const uint64_t k = fine_key<T, D, G, false>(a, q_fine, b, g, j);
         if (lane == 0) keys[j] = k;
       }
       __syncthreads();
@@ -857,12 +866,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
         __syncthreads();
         if (lane == 0) red[warp] = __popc(me);
         __syncthreads();
-        int before = equal + __popc(me & ((1u << lane) - 1));
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) before += red[w];
-          equal += red[w];
-        }
+        const int of = lane < kWarps ? red[lane] : 0;
+        const int before = equal + __popc(me & ((1u << lane) - 1)) + __reduce_add_sync(kFull, lane < warp ? of : 0);
+        equal += __reduce_add_sync(kFull, of);
         const uint32_t m = __ballot_sync(kFull, in || (eq && before < left));
         if (lane == 0 && m) bitmap[j >> 5] |= m;
       }
@@ -885,12 +891,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
     __syncthreads();
     if (lane == 31) red[warp] = at;
     __syncthreads();
-    at += done - n;
-#pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
-      if (x < warp) at += red[x];
-      done += red[x];
-    }
+    const int of = lane < kWarps ? red[lane] : 0;
+    at += done - n + __reduce_add_sync(kFull, lane < warp ? of : 0);
+    done += __reduce_add_sync(kFull, of);
     while (m) {
       if (at < K) out[at] = w * 32 + __ffs(m) - 1;
       ++at;

@@ -187,6 +187,13 @@ def test_refusals():
         plain.write_chunk([0], [2], q, x, x)
     bounded = PagedKVCache(8, HKV, D, BS, torch.bfloat16, 4, key_bounds=True)
     bounded.add(0, 3)
+    for kw in (dict(max_selected=0), dict(max_selected=2, n_first=2, n_last=1), dict(max_selected=4, n_first=-1)):
+        with pytest.raises(ValueError):
+            bounded.decode_step([0], q, x, x, 0.1, **kw)
+    with pytest.raises(ValueError):
+        PagedKVCache(8, HKV, D, BS, torch.bfloat16, 4, rope=Rope(torch.ones(4, device="cuda")))
+    with pytest.raises(ValueError):
+        PagedKVCache(8, HKV, D, BS, torch.bfloat16, 4, rope=Rope(*P.pkv_rope_frequencies(2 * D)))
     with pytest.raises(ValueError):
         bounded.decode_step_host(np.array([0]), q.cpu(), x.cpu(), x.cpu(), 0.1)
     assert bounded.alloc.seq_len(0) == 3

@@ -242,6 +242,16 @@ def test_select_with_nan_and_infinities(dtype):
     check_select(q, bounds, tables, lens, k, bs, 1, 1)
 
 
+def test_select_tiny_values():
+    """Products below 32 bits' range: ranked in 64."""
+    bs, d, k = 16, 64, 10
+    lens = [200 * bs]
+    tables, nb = batch(lens, bs, 5)
+    for dtype, f in (("f32", 1e-30), ("bf16", 1e-30), ("bf16", 1e-20)):
+        bounds = bounds_of(nb, 1, d, dtype, 8) * f
+        check_select(keys((1, 1, d), dtype, 9) * f, bounds, tables, lens, k, bs, 1, 1)
+
+
 def test_select_large_values():
     """Products beyond 32 bits: every candidate is ranked in 64."""
     bs, d, k = 16, 64, 10
