@@ -662,7 +662,8 @@ int pkv_device_status(void* stream, int32_t* status, int32_t clear);
  * the append-and-decode forms), the producer of CTA `cta` skips the copies
  * of that CTA's first work unit, so their consumers wait for chunks that
  * never arrive and give up after the limit; the producer still waits, with
- * the same limit, for every copy it did issue before its CTA exits.  cta < 0
+ * the same limit, for every copy it did issue before its CTA exits.  In the
+ * block-sparse forms the warps of CTA `cta` skip their first chunk.  cta < 0
  * restores normal operation (the default).  Outputs of a stalled call are
  * unspecified; decode does not write the pools.  Process-wide setting, read
  * at each launch; always returns PKV_OK. */

@@ -212,7 +212,7 @@ int sparse_decode(const char* fn, const void* q, const void* k_pool, const void*
   if (sparse_by_cluster(dtype, max_selected)) {
     const double k = dtype == PKV_FP8_E4M3 ? k_scale : 1.0;
     const pkv::SparseDecodeArgs d{a, q, out, static_cast<float>(static_cast<double>(scale) * k * 1.4426950408889634),
-                                  v_scale};
+                                  v_scale, g_stall_cta.load(std::memory_order_relaxed)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool d128 = head_dim == 128;
     switch (dtype) {

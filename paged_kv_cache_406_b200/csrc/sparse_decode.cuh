@@ -115,6 +115,9 @@ struct SparseDecodeArgs {
   const void* q;
   float* out;
   float scale_log2, v_scale;
+  // Test support for the bounded waits (pkv_debug_stall_decode): the warps of
+  // CTA `stall_cta` leave out their first chunk's copies.  < 0 in normal calls.
+  int32_t stall_cta;
 };
 
 template <typename T, int D, int G, int kWarps>
@@ -227,7 +230,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
   };
   if (lane == 0) {
     for (int i = 0; i < kNS; ++i)
-      if (c_first + i * step < chunks) issue(c_first + i * step, i);
+      if (c_first + i * step < chunks && (i > 0 || a.stall_cta != static_cast<int>(blockIdx.x)))
+        issue(c_first + i * step, i);
   }
 
   float acc[kVP][kTiles][4];

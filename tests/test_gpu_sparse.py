@@ -447,6 +447,70 @@ def test_bad_selections_end_the_list_and_are_recorded():
     assert P.pkv_device_status(clear=True) == -1 and bool((out == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_wait_that_runs_out(dtype):
+    """A CTA whose first copies are left out: its waits give up, the call ends
+    with a status, the other rows and the next call are right."""
+    bs, hkv, d = 16, 4, 128
+    lens = [40 * bs, 33 * bs]
+    tables, nb = batch(lens, bs, 3)
+    kp, vp = keys((nb, hkv, bs, d), dtype, 1), keys((nb, hkv, bs, d), dtype, 2)
+    q = keys((2, 2 * hkv, d), "f16" if dtype == "e4m3" else dtype, 3)
+    sel = choose(lens, bs, hkv, 30, 1)
+    args = (q.cuda(), kp.cuda(), vp.cuda(), torch.from_numpy(tables).cuda(),
+            torch.tensor(lens, dtype=torch.int32).cuda(), torch.from_numpy(sel).cuda(), d ** -0.5)
+    call = (lambda: P.pkv_paged_attention_decode_sparse_fp8(*args, 1.0, 1.0)) if dtype == "e4m3" else \
+        (lambda: P.pkv_paged_attention_decode_sparse(*args))
+    want = call().clone()
+    P.pkv_debug_stall_decode(0)
+    try:
+        got = call()
+        assert P.pkv_device_status(clear=True) == -6
+    finally:
+        P.pkv_debug_stall_decode(-1)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[0, 2:], want[0, 2:])  # CTA 0 serves sequence 0, KV head 0
+    assert torch.equal(call(), want)
+
+
+def test_offsets_beyond_32_bits():
+    """Blocks at the end of pools of more than 2^32 bytes (and bounds of more
+    than 2^29 values), through every operator."""
+    bs, hkv, g, d, nb, k = 16, 8, 2, 128, 280000, 6
+    kp, vp = (torch.empty(nb, hkv, bs, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    bounds = torch.empty(nb, hkv, 2, d, dtype=torch.bfloat16, device="cuda")
+    assert kp.numel() > 1 << 32
+    lens = [30 * bs - 5, 40]
+    ids = torch.tensor(np.random.default_rng(1).permutation(200)[:33] + nb - 200)
+    tables = torch.full((2, 30), -1, dtype=torch.int32)
+    tables[0], tables[1, :3] = ids[:30], ids[30:]
+    t, L = tables.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    n = sum(lens)
+    x = keys((n, hkv * (g + 2), d), "bf16", 3).cuda()
+    pos = torch.tensor([p for m in lens for p in range(m)], dtype=torch.int32)
+    slot = torch.tensor([int(tables[b, p // bs]) * bs + p % bs for b, m in enumerate(lens) for p in range(m)])
+    inv, _ = P.pkv_rope_frequencies(d)
+    hq = g * hkv
+    q = P.pkv_rope_append(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], pos.cuda(), inv, slot.to(torch.int32).cuda(),
+                          kp, vp)
+    P.pkv_block_bounds(kp, t, L, bounds, L, max(lens))
+    q = q[[lens[0] - 1, n - 1]].contiguous()
+    sel = P.pkv_block_select(q, bounds, t, L, k, bs, 1, 1)
+    out = P.pkv_paged_attention_decode_sparse(q, kp, vp, t, L, sel, d ** -0.5)
+    # the same in a pool of 200 blocks
+    small = [p[nb - 200:].contiguous() for p in (kp, vp)]
+    st = torch.where(tables >= 0, tables - (nb - 200), tables)
+    want_b, _ = bounds_by_hand(small[0].cpu(), st.numpy(), lens, lens, torch.zeros(200, hkv, 2, d, dtype=torch.bfloat16), bs)
+    used = (ids - (nb - 200)).long()
+    assert torch.equal(bounds[nb - 200:].cpu()[used].float(), want_b[used].float())
+    want_s = select_by_hand(q.cpu(), want_b, st.numpy(), lens, k, bs, 1, 1)
+    assert np.array_equal(sel.cpu().numpy(), want_s)
+    ref = attend_by_hand(q.cpu(), small[0].cpu(), small[1].cpu(), st.numpy(), lens, want_s, d ** -0.5)
+    assert bool(((out.cpu().double() - ref).abs() <= TOL["bf16"] * ref.abs().clamp(min=1)).all())
+    rows = slot - (nb - 200) * bs
+    assert torch.equal(small[1].transpose(1, 2).reshape(-1, hkv, d)[rows.cuda()].view(torch.int16),
+                       x[:, hq + hkv:].contiguous().view(torch.int16))
+
+
 # ---------------------------------------------------------------------------
 # the operators together
 # ---------------------------------------------------------------------------
