@@ -3,7 +3,9 @@
 As in ``binding.py`` every function has the name of the C entry point it
 calls, checks its tensors and forwards pointers, sizes and the stream that is
 current on the tensors' device; the tensors of a call lie on one device, which
-need not be the current one.
+need not be the current one.  A decode step's calls are short, so each function
+checks everything in one expression first and looks for what is wrong only
+where that fails.
 """
 from __future__ import annotations
 
@@ -69,6 +71,15 @@ def _rows(t: torch.Tensor, name: str, dev: int, dtype=None):
     return n, heads, d, s0 if n > 1 else heads * d
 
 
+_I32, _F64 = torch.int32, torch.float64
+_FLOATS = {torch.float32: N.PKV_F32, torch.bfloat16: N.PKV_BF16, torch.float16: N.PKV_F16}
+
+
+def _packed(s, d: int, heads: int) -> bool:
+    """Whether a stride leaves only the token's free."""
+    return s[2] == 1 and (s[1] == d or heads == 1)
+
+
 def _positions(positions: torch.Tensor, inv_freq: torch.Tensor, n: int, dev: int) -> int:
     _on(positions, "positions", dev, torch.int32)
     _on(inv_freq, "inv_freq", dev, torch.float64)
@@ -107,11 +118,20 @@ def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
     stride) by ``positions * inv_freq``; returns ``out`` (``x`` itself for in
     place).  ``transpose`` applies the transposed map, which takes the
     gradient of the result to that of ``x``."""
-    dev = _device(x, "x")
-    n, heads, d, stride = _rows(x, "x", dev)
-    rot = _positions(positions, inv_freq, n, dev)
-    if x.dtype not in _DTYPES or x.dtype in _E4M3:
-        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    code = _FLOATS.get(x.dtype)
+    n, heads, d = x.shape if x.dim() == 3 else (0, 0, 0)
+    dev, st = x.get_device(), x.stride()
+    if not (n and code is not None and dev >= 0 and _packed(st, d, heads) and positions.dtype == _I32
+            and positions.get_device() == dev and positions.is_contiguous() and positions.numel() == n
+            and inv_freq.dtype == _F64 and inv_freq.get_device() == dev and inv_freq.is_contiguous()):
+        dev = _device(x, "x")
+        n, heads, d, stride = _rows(x, "x", dev)
+        _positions(positions, inv_freq, n, dev)
+        if code is None:
+            raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    else:
+        stride = st[0] if n > 1 else heads * d
+    rot = 2 * inv_freq.numel()
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
         ostride = heads * d
@@ -120,30 +140,49 @@ def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
         if (on, oheads, od) != (n, heads, d):
             raise ValueError("out has the wrong shape")
     _issue(lib().pkv_rope, dev, x.data_ptr(), stride, positions.data_ptr(), inv_freq.data_ptr(), n, heads, d, rot,
-           int(interleaved), float(factor), int(transpose), _DTYPES[x.dtype], out.data_ptr(), ostride)
+           bool(interleaved), float(factor), bool(transpose), code, out.data_ptr(), ostride)
     return out
 
 
 def _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, q_dtype):
-    dev = _device(k, "k")
-    n, hkv, d, ks = _rows(k, "k", dev)
-    dtype = k.dtype
-    if v.shape == k.shape and v.stride() == k.stride() and v.dtype == dtype and v.get_device() == dev:
-        vs = ks  # laid out as k is
-    else:
-        n2, hkv2, d2, vs = _rows(v, "v", dev, dtype)
-        if (n2, hkv2, d2) != (n, hkv, d):
-            raise ValueError("k and v differ in shape")
-    nq, hq, dq, qs = _rows(q, "q", dev, dtype)
-    nb, ph, bs, pd = _pools(k_pool, v_pool, dev)
-    if nq != n or dq != d or ph != hkv or pd != d:
-        raise ValueError(f"q, k, v must be [n_tokens, heads, {pd}] with {ph} heads in k and v")
-    rot = _positions(positions, inv_freq, n, dev)
-    _on(slot_mapping, "slot_mapping", dev, torch.int32)
-    if slot_mapping.numel() != n:
-        raise ValueError("slot_mapping must hold one slot per new token")
-    if dtype not in _DTYPES or dtype in _E4M3:
-        raise TypeError(f"q, k, v must be float32, bfloat16 or float16, got {dtype}")
+    """What the rotating appends pass on, checked."""
+    dtype, dev = k.dtype, k.get_device()
+    ks, vs, qs = k.stride(), v.stride(), q.stride()
+    if not (k.dim() == q.dim() == 3 and k_pool.dim() == 4):
+        raise ValueError("q, k, v must be [n_tokens, heads, head_dim], the pools [num_blocks, num_kv_heads, "
+                         "block_size, head_dim]")
+    n, hkv, d = k.shape
+    nq, hq, dq = q.shape
+    nb, ph, bs, pd = k_pool.shape
+    if not (n and dev >= 0 and dtype in _FLOATS and nq == n and dq == d and ph == hkv and pd == d
+            and v.shape == k.shape and v_pool.shape == k_pool.shape and q.dtype == dtype and v.dtype == dtype
+            and v_pool.dtype == k_pool.dtype and q.get_device() == dev and v.get_device() == dev
+            and k_pool.get_device() == dev and v_pool.get_device() == dev and k_pool.is_contiguous()
+            and v_pool.is_contiguous() and _packed(ks, d, hkv) and _packed(vs, d, hkv) and _packed(qs, d, hq)
+            and positions.dtype == _I32 and positions.get_device() == dev and positions.is_contiguous()
+            and positions.numel() == n and slot_mapping.dtype == _I32 and slot_mapping.get_device() == dev
+            and slot_mapping.is_contiguous() and slot_mapping.numel() == n and inv_freq.dtype == _F64
+            and inv_freq.get_device() == dev and inv_freq.is_contiguous()):
+        dev = _device(k, "k")
+        strides = []
+        for t, name in ((k, "k"), (v, "v"), (q, "q")):
+            tn, th, td, stride = _rows(t, name, dev, dtype)
+            if tn != n or td != d or (name == "v" and th != hkv):
+                raise ValueError("q, k and v differ in tokens, head_dim or (k, v) heads")
+            strides.append(stride)
+        ks, vs, qs = ((x,) for x in strides)
+        _pools(k_pool, v_pool, dev)
+        if ph != hkv or pd != d:
+            raise ValueError(f"q, k, v must be [n_tokens, heads, {pd}] with {ph} heads in k and v")
+        _positions(positions, inv_freq, n, dev)
+        _on(slot_mapping, "slot_mapping", dev, _I32)
+        if slot_mapping.numel() != n:
+            raise ValueError("slot_mapping must hold one slot per new token")
+        if dtype not in _FLOATS:
+            raise TypeError(f"q, k, v must be float32, bfloat16 or float16, got {dtype}")
+    elif n == 1:  # a token's stride is anything
+        ks = vs = (hkv * d,)
+        qs = (hq * d,)
     if q_out is None:
         q_out = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
     else:
@@ -152,7 +191,9 @@ def _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_o
             raise ValueError("q_out has the wrong shape")
         if n and q_out.data_ptr() == q.data_ptr():
             raise ValueError("q_out must not be q")
-    return dev, rot, (qs, ks, vs), (nb, hq, hkv, d, bs), q_out
+    return (dev, q.data_ptr(), qs[0], k.data_ptr(), ks[0], v.data_ptr(), vs[0]), positions.data_ptr(), \
+        inv_freq.data_ptr(), slot_mapping.data_ptr(), n, q_out, k_pool.data_ptr(), v_pool.data_ptr(), \
+        (nb, hq, hkv, d, bs, 2 * inv_freq.numel())
 
 
 def pkv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -165,11 +206,10 @@ def pkv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
     head_dim]`` may be views of one projection's output."""
     if k_pool.dtype != k.dtype:
         raise TypeError(f"k is {k.dtype}, the pools are {k_pool.dtype}")
-    dev, rot, (qs, ks, vs), (nb, hq, hkv, d, bs), q_out = _append_args(
-        q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, k.dtype)
-    _issue(lib().pkv_rope_append, dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
-           inv_freq.data_ptr(), slot_mapping.data_ptr(), k.shape[0], q_out.data_ptr(), k_pool.data_ptr(),
-           v_pool.data_ptr(), nb, hq, hkv, d, bs, rot, int(interleaved), float(factor), _DTYPES[k.dtype])
+    rows, pos, inv, slots, n, q_out, kp, vp, sizes = _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool,
+                                                                  v_pool, q_out, k.dtype)
+    _issue(lib().pkv_rope_append, *rows, pos, inv, slots, n, q_out.data_ptr(), kp, vp, *sizes,
+           bool(interleaved), float(factor), _FLOATS[k.dtype])
     return q_out
 
 
@@ -181,22 +221,22 @@ def pkv_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, posit
     code); the returned q is float16."""
     if k_pool.dtype not in _E4M3:
         raise TypeError(f"the pools must hold e4m3 codes, got {k_pool.dtype}")
-    dev, rot, (qs, ks, vs), (nb, hq, hkv, d, bs), q_out = _append_args(
-        q, k, v, positions, inv_freq, slot_mapping, k_pool, v_pool, q_out, torch.float16)
-    _issue(lib().pkv_rope_append_fp8, dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[k.dtype],
-           positions.data_ptr(), inv_freq.data_ptr(), slot_mapping.data_ptr(), k.shape[0], q_out.data_ptr(),
-           k_pool.data_ptr(), v_pool.data_ptr(), nb, hq, hkv, d, bs, rot, int(interleaved), float(factor),
-           float(k_scale), float(v_scale))
+    rows, pos, inv, slots, n, q_out, kp, vp, sizes = _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool,
+                                                                  v_pool, q_out, torch.float16)
+    _issue(lib().pkv_rope_append_fp8, *rows, _FLOATS[k.dtype], pos, inv, slots, n, q_out.data_ptr(), kp, vp, *sizes,
+           bool(interleaved), float(factor), float(k_scale), float(v_scale))
     return q_out
 
 
 def _batch(block_tables: torch.Tensor, seq_lens: torch.Tensor, dev: int):
-    _on(block_tables, "block_tables", dev, torch.int32)
-    _on(seq_lens, "seq_lens", dev, torch.int32)
-    b = seq_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+    b, shape = seq_lens.numel(), block_tables.shape
+    if not (len(shape) == 2 and shape[0] == b and block_tables.dtype == _I32 and seq_lens.dtype == _I32
+            and block_tables.get_device() == dev and seq_lens.get_device() == dev and block_tables.is_contiguous()
+            and seq_lens.is_contiguous()):
+        _on(block_tables, "block_tables", dev, _I32)
+        _on(seq_lens, "seq_lens", dev, _I32)
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and seq_lens [num_seqs]")
-    return b, block_tables.shape[1]
+    return b, shape[1]
 
 
 def pkv_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, bounds: torch.Tensor,
@@ -262,8 +302,8 @@ def pkv_block_select(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.
         _on(workspace, "workspace", dev, torch.uint8)
         ws_bytes = workspace.numel()
     _issue(lib().pkv_block_select, dev, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), b,
-           q.shape[1], hkv, d, nb, maxb, int(block_size), int(max_selected), int(n_first), int(n_last),
-           _dtype_code(bounds), workspace.data_ptr(), ws_bytes, selected.data_ptr())
+           q.shape[1], hkv, d, nb, maxb, int(block_size), int(max_selected), int(n_first),
+           int(n_last), _DTYPES[bounds.dtype], workspace.data_ptr(), ws_bytes, selected.data_ptr())
     return selected
 
 
@@ -290,7 +330,7 @@ def _sparse(fn, q, k_pool, v_pool, block_tables, seq_lens, selected, tail, q_dty
         raise ValueError(f"selected must be [{b}, {hkv}, max_selected]")
     hq, k = q.shape[1], selected.shape[2]
     if out is None:
-        out = torch.empty((b, hq, d), dtype=torch.float32, device=q.device)
+        out = torch.empty_like(q, dtype=torch.float32)  # q is packed
     else:
         _on(out, "out", dev, torch.float32)
         if tuple(out.shape) != (b, hq, d):

@@ -275,3 +275,27 @@ def test_capture_replay_and_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(q_out, -want) and torch.equal(kp, -wk)
+
+
+def test_one_token_of_a_strided_tensor():
+    """A single token's stride may be anything, an odd one among them."""
+    base, pos, inv = inputs(1, 12, 64, 64, "bf16", 3)
+    odd = torch.empty(1 * 777 + 12 * 64, dtype=torch.bfloat16, device="cuda").as_strided((1, 12, 64), (777, 64, 1))
+    odd.copy_(base)
+    assert torch.equal(P.pkv_rope(odd, pos, inv), P.pkv_rope(base, pos, inv))
+    pools = [torch.zeros(1, 3, 8, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    slot = torch.tensor([4], dtype=torch.int32, device="cuda")
+    a = P.pkv_rope_append(odd[:, :6], odd[:, 6:9], odd[:, 9:], pos, inv, slot, pools[0], pools[1])
+    b = P.pkv_rope_append(base[:, :6].contiguous(), base[:, 6:9].contiguous(), base[:, 9:].contiguous(), pos, inv, slot,
+                          pools[2], pools[3])
+    assert torch.equal(a, b) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+
+
+def test_numpy_scalars_and_no_tokens():
+    x, pos, inv = inputs(2, 4, 64, 64, "f32")
+    want = P.pkv_rope(x, pos, inv, factor=0.5)
+    assert torch.equal(P.pkv_rope(x, pos, inv, interleaved=np.bool_(False), factor=np.float32(0.5)), want)
+    assert P.pkv_rope(x[:0], pos[:0], inv).shape == (0, 4, 64)
+    kp = torch.zeros(1, 1, 8, 64, device="cuda")
+    got = P.pkv_rope_append(x[:0, :2], x[:0, 2:3], x[:0, 3:], pos[:0], inv, pos[:0], kp, kp.clone())
+    assert got.shape == (0, 2, 64) and not bool(kp.any())
