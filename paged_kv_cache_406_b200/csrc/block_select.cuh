@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 // selection: score_kernel, then select_kernel with one CTA per (sequence, KV
 // head): 256 threads and four CTAs an SM, or 1024 threads for few long rows (16
 // rows of 8192 blocks: 24.5 us in all against 31; 512 rows of 2048: 71 against
-// 99).  The selection is a chain of short steps on one row (7 us for 512
-// blocks, 12 for 8192) and bound by their latency.
+// 99).  The selection is a chain of short steps on one row (6 us for 512
+// blocks, 11 for 8192) and bound by their latency.
 // ---------------------------------------------------------------------------
 struct TileStats {  // of 16 scores
   uint32_t min_key, max_key;  // the candidates' keys
@@ -224,6 +224,7 @@ struct SelectArgs {
   int32_t max_selected, n_first, n_last;
   int32_t tiles;        // of 16 blocks, in max_blocks
   int32_t smem_scores;  // blocks whose scores fit the shared memory of the launch (0: re-read them)
+  int32_t after_scores; // whether score_kernel is the launch before select_kernel
 };
 
 constexpr int kSelectBins = 1024;
@@ -236,10 +237,9 @@ constexpr int kSelectFine = 512;    // border blocks ranked in shared memory
 // Products below 2^-126 may be lost altogether: 256 of them are below 1e-35.
 constexpr float kScoreError = 1.0f / 16384, kScoreTiny = 1e-35f;
 
-// Blocks of sequence b (0 for a length outside the table's capacity, which is
-// recorded).
-__device__ __forceinline__ int blocks_of(const SelectArgs& a, int b, bool record) {
-  const int L = a.seq_lens[b];
+// Blocks of a sequence of length L (0 for a length outside the table's
+// capacity, which is recorded).
+__device__ __forceinline__ int blocks_of(const SelectArgs& a, int L, bool record) {
   if (L < 0 || L > a.max_blocks * a.block_size) {
     if (record) record_error(PKV_ERR_INVALID_ARG);
     return 0;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectArg
   // time; a short batch then waits for one trip to memory and no barrier.
   constexpr int kPer = 4;
   auto tiles_of = [&](int b) {
-    const int nblk = b < a.num_seqs ? blocks_of(a, b, false) : 0;
+    const int nblk = b < a.num_seqs ? blocks_of(a, a.seq_lens[b], false) : 0;
     return nblk > a.max_selected ? (nblk + 15) / 16 : 0;
   };
   int count[kPer], mine = 0, total = 0;
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectArg
     }
     done += sum;
   }
-  int nblk = blocks_of(a, b, false), tiles = (nblk + 15) / 16;
+  int nblk = blocks_of(a, a.seq_lens[b], false), tiles = (nblk + 15) / 16;
   const int64_t off = p - static_cast<int64_t>(first) * a.num_kv_heads;
   int g = static_cast<int>(off / tiles), t = static_cast<int>(off - static_cast<int64_t>(g) * tiles);
   auto entry = [&](int r) {  // of row gq + 8 r of the tile at hand
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectArg
           g = 0;
           do tiles = tiles_of(++b);  // there is one: p < end
           while (tiles == 0);
-          nblk = blocks_of(a, b, false);
+          nblk = blocks_of(a, a.seq_lens[b], false);
         }
       }
       phys[0] = entry(0);
@@ -674,8 +674,14 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
   __shared__ TileStats warp_stats[kWarps];
   __shared__ double q_fine[G][D];
   __shared__ float q_norm[G];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Behind score_kernel, which lets this grid be scheduled only once everything
+  // before it is complete, q and the lengths may be read (from L2) while the
+  // scores are still being computed.
+  auto wait = [] {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  };
+  if (!a.after_scores) wait();
   const int64_t row = blockIdx.x;
   const int b = static_cast<int>(row / a.num_kv_heads), g = static_cast<int>(row - static_cast<int64_t>(b) * a.num_kv_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -684,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
 #pragma unroll
     for (int d = 0; d < D; d += 32) {
       const float x =
-          widen1<Q>(static_cast<const Q*>(a.q)[(static_cast<int64_t>(b) * a.num_q_heads + g * G + warp) * D + d + lane]);
+          widen1<Q>(__ldcg(static_cast<const Q*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + g * G + warp) * D + d + lane));
       q_fine[warp][d + lane] = x;
       s += fabsf(x);
     }
@@ -692,10 +698,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
     if (lane == 0) q_norm[warp] = s;
   }
-  const int nblk = blocks_of(a, b, g == 0 && tid == 0);
+  const int nblk = blocks_of(a, __ldcg(a.seq_lens + b), g == 0 && tid == 0);
   const int K = a.max_selected;
   int32_t* out = a.selected + row * K;
   if (nblk <= K) {  // every block
+    if (a.after_scores) wait();
     for (int i = tid; i < K; i += kThreads) out[i] = i < nblk ? i : -1;
     return;
   }
@@ -710,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 4) select_ker
     if (i == words - 1 && (nblk & 31)) m &= (1u << (nblk & 31)) - 1;
     bitmap[i] = m;
   }
+  if (a.after_scores) wait();
 
   if (need0 > 0) {
     const float* scores = row_scores;

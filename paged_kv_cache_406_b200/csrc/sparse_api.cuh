@@ -75,6 +75,7 @@ int launch_select(pkv::SelectArgs a, const char* fn, cudaStream_t s) {
     e = launch_pdl(pkv::score_kernel<T, D, G>, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, 2 * sm_count(dev)))),
                    dim3(pkv::kScoreThreads), 0, s, a);
     if (e != cudaSuccess) return cuda_fail(e, fn);
+    a.after_scores = 1;
   }
   a.smem_scores = a.max_blocks <= kSelectSmemScores ? a.max_blocks : 0;
   const size_t smem = static_cast<size_t>((a.max_blocks + 31) / 32 + a.smem_scores) * 4;

@@ -301,8 +301,8 @@ def pkv_block_select(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.
     else:
         _on(workspace, "workspace", dev, torch.uint8)
         ws_bytes = workspace.numel()
-    _issue(lib().pkv_block_select, dev, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), b,
-           q.shape[1], hkv, d, nb, maxb, int(block_size), int(max_selected), int(n_first),
+    _issue(lib().pkv_block_select, dev, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+           b, q.shape[1], hkv, d, nb, maxb, int(block_size), int(max_selected), int(n_first),
            int(n_last), _DTYPES[bounds.dtype], workspace.data_ptr(), ws_bytes, selected.data_ptr())
     return selected
 

@@ -164,9 +164,11 @@ def test_e4m3_cache_and_bounds_refreshed():
     again = PagedKVCache(64, HKV, D, BS, torch.float8_e4m3fn, 32, k_scale=0.25, v_scale=0.25, k_pool=cache.k_pool,
                          v_pool=cache.v_pool)
     t, n = cache.alloc.block_tables([5], 32)
-    q = P.pkv_rope(step[0], torch.tensor([200], dtype=torch.int32, device="cuda"), cache.rope.inv_freq, interleaved=True)
+    at = torch.tensor([200], dtype=torch.int32, device="cuda")
+    q = P.pkv_rope(step[0], at, cache.rope.inv_freq, interleaved=True)
     dense = P.pkv_paged_attention_decode_fp8(q.to(torch.float16), again.k_pool, again.v_pool,
-                                             torch.from_numpy(t).cuda(), torch.from_numpy(n).cuda(), D ** -0.5, 0.25, 0.25)
+                                             torch.from_numpy(t).cuda(), torch.from_numpy(n).cuda(), D ** -0.5, 0.25,
+                                             0.25)
     # q rounded to bf16 first here: half a step 2^-9 of each channel moves a score by about 2^-9 and an output likewise
     assert float((out - dense).abs().max()) <= 0.05
 

@@ -422,7 +422,8 @@ def test_bad_selections_end_the_list_and_are_recorded():
     tables, nb = batch(lens, bs, 3)
     kp, vp = keys((nb, hkv, bs, d), "bf16", 1), keys((nb, hkv, bs, d), "bf16", 2)
     q = keys((1, 2, d), "bf16", 3)
-    dev = (q.cuda(), kp.cuda(), vp.cuda(), torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    dev = (q.cuda(), kp.cuda(), vp.cuda(), torch.from_numpy(tables).cuda(),
+           torch.tensor(lens, dtype=torch.int32).cuda())
 
     def run(sel, t=None):
         a = dev if t is None else (*dev[:3], t, dev[4])
@@ -499,7 +500,8 @@ def test_offsets_beyond_32_bits():
     # the same in a pool of 200 blocks
     small = [p[nb - 200:].contiguous() for p in (kp, vp)]
     st = torch.where(tables >= 0, tables - (nb - 200), tables)
-    want_b, _ = bounds_by_hand(small[0].cpu(), st.numpy(), lens, lens, torch.zeros(200, hkv, 2, d, dtype=torch.bfloat16), bs)
+    blank = torch.zeros(200, hkv, 2, d, dtype=torch.bfloat16)
+    want_b, _ = bounds_by_hand(small[0].cpu(), st.numpy(), lens, lens, blank, bs)
     used = (ids - (nb - 200)).long()
     assert torch.equal(bounds[nb - 200:].cpu()[used].float(), want_b[used].float())
     want_s = select_by_hand(q.cpu(), want_b, st.numpy(), lens, k, bs, 1, 1)
@@ -535,8 +537,9 @@ def test_steps_of_a_long_context(dtype):
     def append(pos, seq):
         n = len(pos)
         x = torch.randn(n, hq + 2 * hkv, d, generator=g, device="cuda").to(io)
-        slots = torch.tensor([int(tables[s, p // bs]) * bs + p % bs for p, s in zip(pos, seq)], dtype=torch.int32).cuda()
-        a = (x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], torch.tensor(pos, dtype=torch.int32).cuda(), inv, slots, kp, vp)
+        slots = torch.tensor([int(tables[s, p // bs]) * bs + p % bs for p, s in zip(pos, seq)], dtype=torch.int32)
+        a = (x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], torch.tensor(pos, dtype=torch.int32).cuda(), inv,
+             slots.cuda(), kp, vp)
         return P.pkv_rope_append_fp8(*a, *scales, factor=factor) if dtype == "e4m3" else \
             P.pkv_rope_append(*a, factor=factor)
 
