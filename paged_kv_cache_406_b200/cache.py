@@ -227,6 +227,17 @@ class PagedKVCache:
                                                             self.k_scale, self.v_scale, out=out)
         return LC.pkv_paged_attention_decode_sparse(q, self.k_pool, self.v_pool, tables, lens, sel, scale, out=out)
 
+    def rotate(self, x: torch.Tensor, positions: torch.Tensor, undo: bool = False) -> torch.Tensor:
+        """Rows ``x`` [n, heads, D] rotated as the cache rotates (``positions``
+        int32 [n] on the device): queries over rows that are in the cache
+        already, as behind a prompt that :meth:`add_cached` found whole.
+        ``undo`` applies the transposed rotation: with a factor of 1 it takes
+        rotated rows back, else it is the map of gradients."""
+        if self.rope is None:
+            raise ValueError("the cache was made without a rotation")
+        r = self.rope
+        return LC.pkv_rope(x, positions, r.inv_freq, r.interleaved, r.factor, undo)
+
     # -- prompts -------------------------------------------------------------
     def write_chunk(self, seq_ids: Sequence[int], n_new: Sequence[int], q: torch.Tensor, k_new: torch.Tensor,
                     v_new: torch.Tensor):

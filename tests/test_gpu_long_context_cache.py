@@ -147,6 +147,34 @@ def test_selecting_every_block_is_the_dense_step():
                        caches[1].k_pool.view(torch.int16)[caches[1].alloc.block_tables([0], 32)[0][0, :18]])
 
 
+def test_queries_over_a_cached_prompt():
+    """A prompt found whole by prefix caching: its rows are in the pool, only
+    the query is rotated, and the attention is the one behind the append."""
+    rope = Rope(*P.pkv_rope_frequencies(128))
+    cache = PagedKVCache(32, HKV, D, BS, torch.bfloat16, 16, rope=rope)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    tokens = np.arange(6 * BS) % 50
+    assert cache.add_cached(0, tokens) == 0
+    q = rand(6 * BS, HQ, D)
+    turned, tables, lens, start = cache.write_chunk([0], [6 * BS], q, rand(6 * BS, HKV, D), rand(6 * BS, HKV, D))
+    assert cache.add_cached(1, tokens) == 6 * BS
+    last = torch.tensor([6 * BS - 1], dtype=torch.int32, device="cuda")
+    again = cache.rotate(q[-1:], last)
+    assert torch.equal(again, turned[-1:])
+    t, n = cache.alloc.block_tables([1], 16)
+    want = P.pkv_paged_attention_decode(turned[-1:].contiguous(), cache.k_pool, cache.v_pool, tables, lens, D ** -0.5)
+    got = P.pkv_paged_attention_decode(again, cache.k_pool, cache.v_pool, torch.from_numpy(t).cuda(),
+                                       torch.from_numpy(n).cuda(), D ** -0.5)
+    assert torch.equal(got, want)
+    back = cache.rotate(again.float(), last, undo=True)
+    # one rounding to bf16 of each rotated channel, and 32-bit rotations
+    size = q[-1:].float().abs()
+    assert bool(((back - q[-1:].float()).abs() <= 2.0 ** -8 * 2 * (size + size.roll(D // 2, -1))).all())
+    with pytest.raises(ValueError):
+        PagedKVCache(4, HKV, D, BS, torch.bfloat16, 4).rotate(again, last)
+
+
 def test_e4m3_cache_and_bounds_refreshed():
     cache = PagedKVCache(64, HKV, D, BS, torch.float8_e4m3fn, 32, k_scale=0.25, v_scale=0.25, key_bounds=True,
                          rope=Rope(*P.pkv_rope_frequencies(64), interleaved=True))
