@@ -24,8 +24,9 @@
 //                  query head) merges the per-partition (m, l, o) with the
 //                  max/sum rescaling
 //                      out = Σ_p 2^(m_p-M) o_p / Σ_p 2^(m_p-M) l_p.
-// Scores are kept in log2 units (q is pre-multiplied by scale·log2 e).  The
-// running max is only moved when a new score exceeds it by more than
+// Scores are kept in log2 units (q is pre-multiplied by scale·log2 e where that
+// shrinks it; a factor above 1, which could take q beyond 32 bits where the score
+// is not, is applied to the score).  The running max is only moved when a new score exceeds it by more than
 // kRescaleThreshold (2^8 headroom in fp32), which leaves the result unchanged
 // because every accumulator and sum is always taken against the same m.
 #pragma once
@@ -447,7 +448,10 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
   for (int w = unit_index(0); w < n_work; w = unit_index(++iter)) {
     const WorkUnit u = load_unit(p, w);
 
-    // q rows of this KV head's G query heads, my dims, scaled to log2 units
+    // q rows of this KV head's G query heads, my dims, scaled to log2 units up
+    // to the factor `rest` (1 for the usual scales)
+    const bool shrinks = fabsf(p.scale_log2) < 1.f;
+    const float fold = shrinks ? p.scale_log2 : 1.f, rest = shrinks ? 1.f : p.scale_log2;
     float2 q2[G][kPairs];
     {
       const T* qrow = static_cast<const T*>(p.q) + (static_cast<int64_t>(u.b) * Hq + u.g * G) * D;
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
           Elem<T>::widen(raw, f);
 #pragma unroll
           for (int e = 0; e < kVec / 2; ++e)
-            q2[h][i * kVec / 2 + e] = make_float2(f[e].x * p.scale_log2, f[e].y * p.scale_log2);
+            q2[h][i * kVec / 2 + e] = make_float2(f[e].x * fold, f[e].y * fold);
         }
       }
     }
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
           for (int h = 0; h < G; ++h) part[h] = pp[h].x + pp[h].y;
         }
         float s_own = reduce_scatter<G>(part, r8);
-        s_own = valid ? s_own : -INFINITY;
+        s_own = valid ? s_own * rest : -INFINITY;
 
         if (__any_sync(kFull, s_own > m_own + kRescaleThreshold)) {
           float mx = s_own;
