@@ -219,7 +219,9 @@ int pkv_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num
  * physical block block_tables[b][t / block_size] at offset t % block_size.
  * No mask: the decode query is the newest position and sees every cached
  * token (call pkv_kv_append first to include the new token itself).
- * seq_lens[b] == 0 gives zeros.
+ * seq_lens[b] == 0 gives zeros.  A token that scores -inf (an infinite key,
+ * a product below 32 bits' range) has weight 0; nothing but such tokens gives
+ * zeros.  The same holds in every other attention call below.
  *
  * q: dtype[num_seqs][num_q_heads][head_dim]; block_tables:
  * int32[num_seqs][max_blocks_per_seq]; seq_lens: int32[num_seqs], each in

@@ -297,13 +297,11 @@ __device__ __forceinline__ void merge_store(const float* rec, const WorkUnit& u,
 #pragma unroll
     for (int w2 = 0; w2 < kCW; ++w2) M = fmaxf(M, rec[w2 * kMF + G * D + h]);
     float num = 0.f, den = 0.f;
-    if (M != -INFINITY) {
 #pragma unroll
-      for (int w2 = 0; w2 < kCW; ++w2) {
-        const float f = fast_exp2(rec[w2 * kMF + G * D + h] - M);
-        num += f * rec[w2 * kMF + h * D + d];
-        den += f * rec[w2 * kMF + G * D + G + h];
-      }
+    for (int w2 = 0; w2 < kCW; ++w2) {
+      const float f = fast_exp2(rec[w2 * kMF + G * D + h] - M);
+      num += f * rec[w2 * kMF + h * D + d];
+      den += f * rec[w2 * kMF + G * D + G + h];
     }
     const int64_t row = static_cast<int64_t>(u.b) * p.num_q_heads + u.g * G + h;
     if (single) {
@@ -473,11 +471,11 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
     float2 acc[G][kPairs];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      m[h] = -INFINITY;
+      m[h] = kLowest;
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) acc[h][e] = make_float2(0.f, 0.f);
     }
-    float m_own = -INFINITY, l_own = 0.f;
+    float m_own = kLowest, l_own = 0.f;
 
     const int j0 = (warp - static_cast<int>(c % kConsumerWarps) + kConsumerWarps) % kConsumerWarps;
     int s = (c + j0) % NS;
@@ -530,7 +528,7 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             const float mn = fmaxf(m[h], mall[h]);
-            fac[h] = (mn == -INFINITY) ? 1.f : fast_exp2(m[h] - mn);
+            fac[h] = fast_exp2(m[h] - mn);
             m[h] = mn;
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) acc[h][e] = __fmul2_rn(acc[h][e], make_float2(fac[h], fac[h]));

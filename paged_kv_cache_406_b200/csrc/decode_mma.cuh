@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     float acc[kSteps][4];
 #pragma unroll
     for (int mt = 0; mt < kSteps; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2tq, 2tq+1
+    float m0 = kLowest, m1 = kLowest, l0 = 0.f, l1 = 0.f;  // heads 2tq, 2tq+1
 
     const int k0 = (warp - static_cast<int>(c % kCW) + kCW) % kCW;
     int s = (c + k0) % NS;
@@ -292,8 +292,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, o));
         }
         const float n0 = fmaxf(m0, bm0), n1 = fmaxf(m1, bm1);
-        const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
-        const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
+        const float f0 = fast_exp2(m0 - n0), f1 = fast_exp2(m1 - n1);
 #pragma unroll
         for (int mt = 0; mt < kSteps; ++mt) {
           acc[mt][0] *= f0;

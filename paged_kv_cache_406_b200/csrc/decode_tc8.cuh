@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(t8::kThreads, NSt <= 2 ? 3 : (NSt == 3 ? 2 : 1
       float m[G], l[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        m[h] = -INFINITY;
+        m[h] = kLowest;
         l[h] = 0.f;
       }
       for (int c = 0; c < nc; ++c, ++j) {
@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(t8::kThreads, NSt <= 2 ? 3 : (NSt == 3 ? 2 : 1
           const float* rr = red + (j & 1) * 32 + h;
           const float mc = fmaxf(fmaxf(rr[0], rr[8]), fmaxf(rr[16], rr[24]));
           f[h] = 1.f;
-          if (mc > m[h] + t8::kThreshold) {  // also when m is still -inf
-            f[h] = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mc);
+          if (mc > m[h] + t8::kThreshold) {  // also when m is still kLowest: f = 0
+            f[h] = fast_exp2(m[h] - mc);
             m[h] = mc;
             resc = resc || c > 0;
           }

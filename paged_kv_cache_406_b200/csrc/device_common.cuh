@@ -227,6 +227,11 @@ __device__ __forceinline__ int32_t ld_table(const int32_t* p, uint64_t policy) {
   return v;
 }
 
+// Where a running maximum of scores starts: no finite score is lower, and it is
+// finite, so a score of -inf (an infinite key, a product that overflows) met
+// before any other still gets the weight 2^(-inf - kLowest) = 0.
+constexpr float kLowest = -3.402823466e+38f;
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

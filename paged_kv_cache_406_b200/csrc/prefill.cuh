@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       const int nc = d.nc, L = d.L, n = d.n, tok0 = d.tok0, pos_min = d.pos_min;
       const int tok = tok0 + R / G;
       const int pos = min(d.ctx + tok, L - 1);  // rows past the chunk end compute a copy of the last row
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = kLowest, l = 0.f;
       for (int j = 0; j < nc && ok; ++j) {
         const int gj = gc + j;           // chunk of the CTA
         const int s = gj % pf::kStages;  // K / V stage
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         float factor = 1.f;
         bool resc = false;
         if (j == 0) {
-          m_used = mc;  // key 0 is visible to every row: finite
+          m_used = fmaxf(mc, kLowest);  // key 0 is visible to every row, but its score may be -inf
         } else if (mc > m_used + pf::kRescale) {
           factor = fast_exp2(m_used - mc);
           m_used = mc;
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       // parked row k sits at slot c ^ (k mod 8), so the parking and the
       // row-wise reads are both free of bank conflicts.  Once the last
       // columns are loaded, O may be overwritten by the next tile's P·V.
-      const float inv = 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // no weight at all: zeros
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];

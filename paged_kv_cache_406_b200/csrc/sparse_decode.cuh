@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
   for (int i = 0; i < kVP; ++i)
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
-  float m = -INFINITY, l = 0.f;  // of head gq
+  float m = kLowest, l = 0.f;  // of head gq
   int stage = 0;
   uint32_t phase = 0;
   for (int c = c_first; c < chunks; c += step) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
     if (__any_sync(kFull, bm > m + kRescaleThreshold)) {
       bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
       bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
-      const float nm = fmaxf(m, bm), f = nm == -INFINITY ? 1.f : fast_exp2(m - nm);
+      const float nm = fmaxf(m, bm), f = fast_exp2(m - nm);
       m = nm;
       l *= f;
       const float f0 = __shfl_sync(kFull, f, 8 * tq), f1 = __shfl_sync(kFull, f, 8 * tq + 4);  // heads 2 tq, 2 tq + 1
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, rec[w * kRec + G * D + h]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mh[w] = top == -INFINITY ? 0.f : fast_exp2(rec[w * kRec + G * D + h] - top);
+    for (int w = 0; w < kWarps; ++w) mh[w] = fast_exp2(rec[w * kRec + G * D + h] - top);
     return top;
   };
   for (int e = tid * 4; e < G * D; e += kThreads * 4) {
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
                      : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
                      : "r"(remote(&rec[e], r))
                      : "memory");
-        const float f = top == -INFINITY ? 0.f : fast_exp2(cm[r] - top);
+        const float f = fast_exp2(cm[r] - top);
         den += f * cl;
         o.x += f * y.x;
         o.y += f * y.y;
