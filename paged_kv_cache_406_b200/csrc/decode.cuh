@@ -59,6 +59,7 @@ struct DecodeParams {
   int32_t num_q_heads, num_kv_heads, partition_tokens, max_parts;
   int32_t n_stages;
   float scale_log2;
+  float q_scale, s_scale;  // decode_kernel: what q and the scores are multiplied by, scale_log2 in all
   float v_scale;  // multiplies the output (e4m3 V pools; 1 otherwise)
   const int4* items;  // {b, partition, partitions of b, end token}
   const int32_t* n_items;
@@ -446,10 +447,7 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
   for (int w = unit_index(0); w < n_work; w = unit_index(++iter)) {
     const WorkUnit u = load_unit(p, w);
 
-    // q rows of this KV head's G query heads, my dims, scaled to log2 units up
-    // to the factor `rest` (1 for the usual scales)
-    const bool shrinks = fabsf(p.scale_log2) < 1.f;
-    const float fold = shrinks ? p.scale_log2 : 1.f, rest = shrinks ? 1.f : p.scale_log2;
+    // q rows of this KV head's G query heads, my dims, scaled to log2 units up to s_scale
     float2 q2[G][kPairs];
     {
       const T* qrow = static_cast<const T*>(p.q) + (static_cast<int64_t>(u.b) * Hq + u.g * G) * D;
@@ -462,7 +460,7 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
           Elem<T>::widen(raw, f);
 #pragma unroll
           for (int e = 0; e < kVec / 2; ++e)
-            q2[h][i * kVec / 2 + e] = make_float2(f[e].x * fold, f[e].y * fold);
+            q2[h][i * kVec / 2 + e] = make_float2(f[e].x * p.q_scale, f[e].y * p.q_scale);
         }
       }
     }
@@ -517,7 +515,7 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodePara
           for (int h = 0; h < G; ++h) part[h] = pp[h].x + pp[h].y;
         }
         float s_own = reduce_scatter<G>(part, r8);
-        s_own = valid ? s_own * rest : -INFINITY;
+        s_own = valid ? s_own * p.s_scale : -INFINITY;
 
         if (__any_sync(kFull, s_own > m_own + kRescaleThreshold)) {
           float mx = s_own;

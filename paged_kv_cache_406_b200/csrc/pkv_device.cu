@@ -559,6 +559,9 @@ int decode_16(const char* fn, const void* q, const void* k_pool, const void* v_p
   p.partition_tokens = pt;
   p.max_parts = w.max_parts;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  const bool shrinks = std::fabs(p.scale_log2) < 1.0f;
+  p.q_scale = shrinks ? p.scale_log2 : 1.0f;
+  p.s_scale = shrinks ? 1.0f : p.scale_log2;
   p.v_scale = 1.0f;
   p.items = reinterpret_cast<const int4*>(ws + w.items);
   p.n_items = reinterpret_cast<const int32_t*>(ws);
