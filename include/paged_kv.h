@@ -630,7 +630,11 @@ int pkv_sparse_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num
  * token of a sequence are not used, whatever they hold.  A length outside the
  * table is recorded as PKV_ERR_INVALID_ARG and gives zeros, a block id outside
  * the pool as PKV_ERR_BAD_BLOCK (block 0 is read instead).  fp32 pools: up to
- * 4 query heads per KV head.  workspace: at least
+ * 4 query heads per KV head.  Weights enter the product with V with 22 bits or
+ * more, small ones beside a large one included; max_selected above 1024 takes
+ * the dense decode's weights (bf16 pools: 16 bits; f16 and e4m3: to 2^-22 of
+ * the row's largest).  The sum of weight (largest 1) times |V| must stay below
+ * 2^120, which only fp32 and bf16 values can exceed.  workspace: at least
  * pkv_sparse_workspace_size() bytes, 256-byte aligned, scratch for the
  * duration of the call. */
 int pkv_paged_attention_decode_sparse(const void* q, const void* k_pool, const void* v_pool,

@@ -84,8 +84,18 @@ __global__ void __launch_bounds__(256) expand_selection_kernel(const SparseArgs 
 // share, and of V rows 2t, 2t + 1, 2t + 8, 2t + 9, whose halves exchanged
 // (prmt) are A fragments of O^T in an order of channels undone at the end.
 // S leaves each lane with head q at tokens 2t, 2t + 1, 2t + 8, 2t + 9: P's B
-// fragments as they are.  P enters as a sum of two f16 or three bf16 values
-// (22 or 24 bits), so its rounding does not show in a 32-bit result.
+// fragments as they are.
+//
+// P enters as a sum of three bf16 values (24 bits at any size; weights are at
+// most 1, since a bf16 value times more could leave 32 bits' range) or of two
+// f16 ones.  f16 steps by 2^-24 however small a value is, so for f16 the unit of
+// the weights follows the scores down as well as up: the largest weight of a
+// lane's four tokens lies between 1 and 2^15, or, where the chunk's tokens
+// differ by more, its largest weight at 2^15.  A weight keeps 22 bits, or 2^-25
+// of its lane's largest, or 2^-40 of its chunk's, down to 2^-60 of the row's
+// largest.  Against the row's largest alone, weights e^-12 below a sink token of
+// value 0 gave an output off by 8e-4 of itself, weights e^-18 below one off by
+// nearly all of it.  The unit is a whole power of two, so moving it is exact.
 //
 // 512 rows of 64 bf16 blocks of 16 tokens (268 MB): 47.7 us, 5.6 TB/s; the
 // dense kernels on the selection as a batch of its own take 52 to 56, loads
@@ -120,6 +130,11 @@ struct SparseDecodeArgs {
   int32_t stall_cta;
 };
 
+// 2^e of a whole e; 0 below 2^-126.
+__device__ __forceinline__ float exp2_whole(float e) {
+  return __int_as_float((__float2int_rn(fminf(fmaxf(e, -127.f), 127.f)) + 127) << 23);
+}
+
 template <typename T, int D, int G, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1)
     sparse_decode_kernel(const SparseDecodeArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -131,7 +146,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
   constexpr int kKP = kRow / 64, kVP = kRow / 128;       // pieces of a K row (four lanes) and a V row (eight lanes)
   constexpr int kSteps = kFp8 ? 4 : 2;                   // mma steps of a K piece
   constexpr int kTiles = kFp8 ? 8 : 4;                   // channel pairs of a V piece
-  constexpr int kTerms = std::is_same_v<Q, __nv_bfloat16> ? 3 : 2;
+  constexpr bool kBf16 = std::is_same_v<Q, __nv_bfloat16>;
+  constexpr int kTerms = kBf16 ? 3 : 2;
   extern __shared__ unsigned char sparse_raw[];
   __shared__ int32_t list[kSparseList];
   __shared__ int32_t first_bad;
@@ -239,7 +255,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
   for (int i = 0; i < kVP; ++i)
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
-  float m = kLowest, l = 0.f;  // of head gq
+  float m = kLowest, l = 0.f, top = kLowest;  // of head gq; m is whole; top: the largest score where m was moved
   int stage = 0;
   uint32_t phase = 0;
   for (int c = c_first; c < chunks; c += step) {
@@ -278,12 +294,23 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
       const int token = 2 * tq + (k & 1) + 8 * (k >> 1);
       x[k] = token < nv ? s[k >> 1][k & 1] * a.scale_log2 : -INFINITY;
     }
-    // ---- online softmax (the running maximum moves only by more than the threshold) ----
+    // ---- online softmax: weights, sums and outputs in units of 2^m ----
     float bm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    if (__any_sync(kFull, bm > m + kRescaleThreshold)) {
+    const bool stay = kBf16 ? bm <= m : bm >= m && bm <= __fadd_rd(m, 15.f);
+    if (!__all_sync(kFull, stay)) {
+      const float own = bm;
       bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
-      bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
-      const float nm = fmaxf(m, bm), f = fast_exp2(m - nm);
+      bm = ceilf(fmaxf(fmaxf(bm, __shfl_xor_sync(kFull, bm, 2)), kLowest));  // of head gq
+      float nm;
+      if constexpr (kBf16) {
+        nm = bm > m ? bm + kRescaleThreshold : m;
+      } else {
+        top = fmaxf(top, bm);
+        // some lane far below the chunk's largest: as many bits for it as there are
+        const float up = __any_sync(kFull, own < bm - 7.f) ? -15.f : -7.f;
+        nm = fmaxf(__fadd_ru(bm, up), top - 60.f);
+      }
+      const float f = exp2_whole(m - nm);
       m = nm;
       l *= f;
       const float f0 = __shfl_sync(kFull, f, 8 * tq), f1 = __shfl_sync(kFull, f, 8 * tq + 4);  // heads 2 tq, 2 tq + 1
