@@ -22,6 +22,7 @@ pkv_paged_attention_decode_sparse): the ``max_selected`` of a decode step.
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -171,6 +172,9 @@ class PagedKVCache:
         if max_selected is not None and (n_first < 0 or n_last < 0 or max_selected < max(1, n_first + n_last)):
             raise ValueError("n_first + n_last must be at most max_selected, which must be positive")
         n = len(seq_ids)
+        if self.rope is not None or self.bounds is not None:
+            q, k_new, v_new = (t.to(self.device, non_blocking=True) for t in (q, k_new, v_new))
+            self._check_step(n, q, k_new, v_new, scale, out, max_selected, partition_tokens)
         ncow, _ = self.prepare_step(seq_ids)
         slots, lens, cow, tables = self.upload_step(n)
         q, k_new, v_new = (t.to(self.device, non_blocking=True) for t in (q, k_new, v_new))
@@ -199,6 +203,40 @@ class PagedKVCache:
                                                partition_tokens=partition_tokens)
         return B.pkv_append_and_decode(k_new, v_new, slots, q, self.k_pool, self.v_pool, tables, lens, scale,
                                        out=out, workspace=ws, partition_tokens=partition_tokens)
+
+    def _check_step(self, n, q, k_new, v_new, scale, out, max_selected, partition_tokens) -> None:
+        """What the calls of a step with rotation or key bounds would refuse one
+        after the other, refused before a slot is reserved or a row written."""
+        if not math.isfinite(scale):
+            raise ValueError("scale is not finite")
+        hkv, d = self.num_kv_heads, self.head_dim
+        floats = (torch.float32, torch.bfloat16, torch.float16)
+        for t, name, heads in ((q, "q", None), (k_new, "k_new", hkv), (v_new, "v_new", hkv)):
+            if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+                raise ValueError(f"{name} must be [{n}, {heads or 'num_q_heads'}, {d}], got {tuple(t.shape)}")
+            if self.fp8 and (self.rope is not None or heads):  # rows of one floating type, quantised on the way
+                ok = t.dtype in floats and (t.dtype == k_new.dtype)
+            else:
+                ok = t.dtype == (torch.float16 if self.fp8 else self.k_pool.dtype)
+            if not ok:
+                raise TypeError(f"{name} is {t.dtype}, the pools are {self.k_pool.dtype}")
+            s0, s1, s2 = t.stride()
+            if self.rope is None:
+                packed = t.is_contiguous()
+            else:  # the token's stride is free
+                packed = s2 == 1 and (s1 == d or t.shape[1] == 1) and (
+                    n <= 1 or (s0 >= t.shape[1] * d and s0 * t.element_size() % 16 == 0))
+            if not packed or t.data_ptr() % 16:
+                raise ValueError(f"{name} must be packed and 16-byte aligned"
+                                 + ("" if self.rope is None else " (its token stride is free)"))
+        if out is not None and (tuple(out.shape) != tuple(q.shape) or out.dtype != torch.float32 or not out.is_contiguous()
+                                or out.get_device() != self.k_pool.get_device()):
+            raise ValueError("out must be a contiguous float32 tensor of q's shape on the cache's device")
+        # head counts and types that the attention does not take
+        LC.pkv_sparse_workspace_size(n, q.shape[1], hkv, d, 1 if max_selected is None else int(max_selected),
+                                     self.block_size, self.k_pool.dtype)
+        if max_selected is None:
+            B.pkv_decode_workspace_size(n, q.shape[1], hkv, d, self.max_blocks, self.block_size, partition_tokens)
 
     def _append(self, q, k_new, v_new, slots, positions) -> torch.Tensor:
         """K and V into their slots, rotated if the cache rotates; returns q as
