@@ -66,7 +66,7 @@ def _rows(t: torch.Tensor, name: str, dev: int, dtype=None):
         raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
     n, heads, d = t.shape
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+    if t.numel() and ((s2 != 1 and d > 1) or (s1 != d and heads > 1)):
         raise ValueError(f"the heads and channels of {name} must be packed (only the token stride is free)")
     return n, heads, d, s0 if n > 1 else heads * d
 

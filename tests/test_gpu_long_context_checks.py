@@ -111,3 +111,14 @@ def test_partition_sizes_and_rows_on_the_host():
     cache.add(1, 5)
     out = cache.decode_step([0, 1], wide[:, :8], wide[:, 8:10], wide[:, 10:], 0.1)
     assert out.shape == (2, 8, D) and cache.alloc.seq_len(0) == 6
+
+
+def test_no_tokens_of_any_stride():
+    """A tensor without elements has no stride to refuse (torch gives some zeros)."""
+    inv, _ = P.pkv_rope_frequencies(64)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    x = torch.zeros(1, 1, 1, device="cuda")[:0].expand(0, 4, 64)
+    assert x.stride() == (0, 0, 0) or x.stride(1) == 0
+    assert P.pkv_rope(x, none, inv).shape == (0, 4, 64)
+    pools = [torch.zeros(1, 4, 8, 64, device="cuda") for _ in range(2)]
+    assert P.pkv_rope_append(x, x, x, none, inv, none, *pools).shape == (0, 4, 64)
