@@ -111,13 +111,34 @@ def pkv_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "pl
     return torch.tensor(list(out), dtype=torch.float64, device=device), factor.value
 
 
+class _Rotation(torch.autograd.Function):
+    """pkv_rope of a tensor that requires a gradient: the transposed map takes
+    the gradient back, by another call (so it can be differentiated in turn)."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, interleaved, factor, transpose):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = interleaved, factor, transpose
+        return pkv_rope(x, positions, inv_freq, interleaved, factor, transpose)
+
+    @staticmethod
+    def backward(ctx, grad):
+        interleaved, factor, transpose = ctx.how
+        return pkv_rope(grad.contiguous(), *ctx.saved_tensors, interleaved, factor, not transpose), *(None,) * 5
+
+
 def pkv_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
              factor: float = 1.0, transpose: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotates the first ``2 * len(inv_freq)`` channels of every head of ``x``
     ``[n_tokens, heads, head_dim]`` (float32, bfloat16 or float16; any token
     stride) by ``positions * inv_freq``; returns ``out`` (``x`` itself for in
     place).  ``transpose`` applies the transposed map, which takes the
-    gradient of the result to that of ``x``."""
+    gradient of the result to that of ``x``; autograd calls it where ``x``
+    requires a gradient (``out`` must then be None; ``inv_freq`` gets none)."""
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise RuntimeError("pkv_rope with out records no gradient, and x requires one: call it under torch.no_grad()")
+        return _Rotation.apply(x, positions, inv_freq, interleaved, factor, transpose)
     code = _FLOATS.get(x.dtype)
     n, heads, d = x.shape if x.dim() == 3 else (0, 0, 0)
     dev, st = x.get_device(), x.stride()
@@ -203,7 +224,8 @@ def pkv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
     """:func:`pkv_kv_append` with the rotation of :func:`pkv_rope` on the way:
     K rotated and V as it is into their slots (``slot < 0`` = padding), q
     rotated into ``q_out``, which is returned.  q, k, v ``[n_tokens, heads,
-    head_dim]`` may be views of one projection's output."""
+    head_dim]`` may be views of one projection's output.  Like every call that
+    writes or reads a pool it records no gradient."""
     if k_pool.dtype != k.dtype:
         raise TypeError(f"k is {k.dtype}, the pools are {k_pool.dtype}")
     rows, pos, inv, slots, n, q_out, kp, vp, sizes = _append_args(q, k, v, positions, inv_freq, slot_mapping, k_pool,
