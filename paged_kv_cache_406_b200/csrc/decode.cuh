@@ -306,7 +306,7 @@ __device__ __forceinline__ void merge_store(const float* rec, const WorkUnit& u,
     }
     const int64_t row = static_cast<int64_t>(u.b) * p.num_q_heads + u.g * G + h;
     if (single) {
-      p.out[row * D + d] = den > 0.f ? p.v_scale * num / den : 0.f;
+      p.out[row * D + d] = den == 0.f ? 0.f : p.v_scale * num / den;  // NaN stays NaN
     } else {
       const int64_t pr = row * p.max_parts + u.part;
       p.part_o[pr * D + d] = p.v_scale * num;
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const int32_t* __restrict__ 
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   float* dst = out + static_cast<int64_t>(row) * D + lane * kPer;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) dst[i] = acc[i] * inv;
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(256) merge_wide_kernel(const int32_t* __restri
 #pragma unroll
     for (int i = 0; i < kPer; ++i) res[i] += f * rec_o[w][lane * kPer + i];
   }
-  const float inv = dt > 0.f ? 1.f / dt : 0.f;
+  const float inv = dt == 0.f ? 0.f : 1.f / dt;
   float* dst = out + static_cast<int64_t>(row) * D + lane * kPer;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) dst[i] = res[i] * inv;

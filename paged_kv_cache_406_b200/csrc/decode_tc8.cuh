@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(t8::kThreads, NSt <= 2 ? 3 : (NSt == 3 ? 2 : 1
         for (int term = t8::kTermsP - 1; term >= 0; --term) num = num * 0.0625f + __uint_as_float(o[term * G + h]);
         const int64_t row = row0 + h;
         if (single) {
-          p.out[row * t8::kD + t] = lt > 0.f ? p.v_scale * num / lt : 0.f;
+          p.out[row * t8::kD + t] = lt == 0.f ? 0.f : p.v_scale * num / lt;  // NaN stays NaN
         } else {
           const int64_t pr = row * p.max_parts + u.part;
           p.part_o[pr * t8::kD + t] = p.v_scale * num;

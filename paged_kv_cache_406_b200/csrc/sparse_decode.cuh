@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
         o.w += f * y.w;
       }
     }
-    const float inv = den > 0.f ? a.v_scale / den : 0.f;
+    const float inv = den == 0.f ? 0.f : a.v_scale / den;
     *reinterpret_cast<float4*>(a.out + row * G * D + e) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   }
   // no CTA leaves while another reads its record
