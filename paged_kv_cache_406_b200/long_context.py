@@ -325,7 +325,7 @@ def pkv_block_select(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.
         ws_bytes = workspace.numel()
     _issue(lib().pkv_block_select, dev, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
            b, q.shape[1], hkv, d, nb, maxb, int(block_size), int(max_selected), int(n_first),
-           int(n_last), _DTYPES[bounds.dtype], workspace.data_ptr(), ws_bytes, selected.data_ptr())
+           int(n_last), _dtype_code(bounds), workspace.data_ptr(), ws_bytes, selected.data_ptr())
     return selected
 
 
@@ -334,6 +334,8 @@ def pkv_sparse_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int
                               block_size: int, dtype: torch.dtype) -> int:
     """Workspace bytes of the block-sparse decode over pools of ``dtype`` (0
     where it needs none)."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; expected float32, bfloat16, float16 or e4m3 codes")
     out = ctypes.c_size_t(0)
     check(lib().pkv_sparse_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_selected, block_size,
                                           _DTYPES[dtype], ctypes.byref(out)))
