@@ -68,13 +68,17 @@ def test_a_refused_step_reserves_and_writes_nothing(what, pool, rope, bounds, ma
     args = change(*step_inputs(rows))
     if pool == torch.float32 and what == "16 heads a group":
         args = (torch.cat(list(step_inputs(rows)[:1]) * 2, 1), *args[1:])  # fp32 pools: 8 are too many already
+    scale = kw.pop("scale", 0.1)
     with pytest.raises(error):
-        cache.decode_step([0, 1], *args, kw.pop("scale", 0.1), max_selected=max_selected, **kw)
+        cache.decode_step([0, 1], *args, scale, max_selected=max_selected, **kw)
     assert cache.alloc.seq_len(0) == 5 and cache.alloc.seq_len(1) == 16 and cache.stats() == free
     for p in (cache.k_pool, cache.v_pool):
         assert bool((p.view(torch.uint8) == 9).all())
     good = cache.decode_step([0, 1], *step_inputs(rows), 0.1, max_selected=max_selected)
     assert good.shape == (2, 8, D) and cache.alloc.seq_len(1) == 17
+    with pytest.raises(error):  # as well behind a step of the same sizes
+        cache.decode_step([0, 1], *args, scale, max_selected=max_selected, **kw)
+    assert cache.alloc.seq_len(0) == 6 and cache.alloc.seq_len(1) == 17
 
 
 def test_a_step_from_views_of_one_projection():
