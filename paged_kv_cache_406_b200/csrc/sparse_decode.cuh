@@ -296,14 +296,14 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
     }
     // ---- online softmax: weights, sums and outputs in units of 2^m ----
     float bm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    const bool stay = kBf16 ? bm <= m : bm >= m && bm <= __fadd_rd(m, 15.f);
+    const bool stay = kBf16 ? bm <= m + kRescaleThreshold : bm >= m && bm <= __fadd_rd(m, 15.f);
     if (!__all_sync(kFull, stay)) {
       const float own = bm;
       bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
       bm = ceilf(fmaxf(fmaxf(bm, __shfl_xor_sync(kFull, bm, 2)), kLowest));  // of head gq
       float nm;
       if constexpr (kBf16) {
-        nm = bm > m ? bm + kRescaleThreshold : m;
+        nm = fmaxf(m, bm);
       } else {
         top = fmaxf(top, bm);
         // some lane far below the chunk's largest: as many bits for it as there are
@@ -328,6 +328,10 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == kSparseFewWarps ? 4 : 1
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float p0 = fast_exp2(x[2 * r] - m), p1 = fast_exp2(x[2 * r + 1] - m);
+      if constexpr (kBf16) {  // at most 2^kRescaleThreshold so far
+        p0 *= 0.00390625f;
+        p1 *= 0.00390625f;
+      }
       l += p0 + p1;
 #pragma unroll
       for (int t = 0; t < kTerms; ++t) {
