@@ -200,10 +200,13 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 
 // ---------------------------------------------------------------------------
 // selection: score_kernel, then select_kernel with one CTA per (sequence, KV
-// head): 256 threads and four CTAs an SM, or 1024 threads for few long rows (16
-// rows of 8192 blocks: 24.5 us in all against 31; 512 rows of 2048: 71 against
-// 99).  The selection is a chain of short steps on one row (6 us for 512
-// blocks, 11 for 8192) and bound by their latency.
+// head): 256 threads and four CTAs an SM, or 1024 threads for few long rows.
+// Measured with the score kernel before the selection started under it, 256
+// against 1024 threads: 16 rows of 8192 blocks 31 us against 24.5, 512 rows of
+// 2048 blocks 71 against 99 (now 20.7 and 69.8 us).  The selection is a chain of short
+// steps on one row (6 us for 512 blocks, 11 for 8192) and bound by their
+// latency.  With eight heads of 128 it spills (up to 52 bytes stored and 148
+// loaded a thread, in the 64-bit scores of the border).
 // ---------------------------------------------------------------------------
 struct TileStats {  // of 16 scores
   uint32_t min_key, max_key;  // the candidates' keys
@@ -230,10 +233,12 @@ struct SelectArgs {
 constexpr int kSelectBins = 1024;
 constexpr int kSelectFine = 512;    // border blocks ranked in shared memory
 
-// Error bound of a 32-bit score over sum_d |q_d| times the largest |bound|.
+// Error taken for a 32-bit score, over sum_d |q_d| times the largest |bound|.
 // 32-bit sums of 2 D = 256 products lose at most 256 x 2^-24 = 2^-16 of that.
-// Tensor cores align the 16 products and the sum of a step to the largest of
-// them and drop bits below 2^-23 of it: 17 x 2^-23 a step, 16 steps, 2^-14.9.
+// How tensor cores sum is not documented; this assumes that they align the 16
+// products and the sum of a step to the largest of them and drop bits below
+// 2^-23 of it: 17 x 2^-23 a step, 16 steps, 2^-14.9.  Measured on sums that
+// grow large and cancel, and on normal ones: 2^-24.7 at most.
 // Products below 2^-126 may be lost altogether: 256 of them are below 1e-35.
 constexpr float kScoreError = 1.0f / 16384, kScoreTiny = 1e-35f;
 
