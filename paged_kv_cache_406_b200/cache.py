@@ -220,7 +220,9 @@ class PagedKVCache:
             a, b, c = q.stride(), k_new.stride(), v_new.stride()
             packed = len(a) == len(b) == len(c) == 3 and a[1:] == b[1:] == c[1:] == (d, 1) and a[0] >= hq * d and \
                 b[0] >= hkv * d and c[0] >= hkv * d and not (a[0] | b[0] | c[0]) & 7
-        if (packed and sizes in self._steps_seen and out is None and q.shape == (n, hq, d)
+        good_out = out is None or (out.shape == q.shape and out.dtype == torch.float32 and out.is_contiguous()
+                                   and out.get_device() == self.k_pool.get_device() and out.data_ptr() % 16 == 0)
+        if (packed and good_out and sizes in self._steps_seen and q.shape == (n, hq, d)
                 and k_new.shape == v_new.shape == (n, hkv, d) and math.isfinite(scale)
                 and not (q.data_ptr() | k_new.data_ptr() | v_new.data_ptr()) & 15):
             return
@@ -245,9 +247,8 @@ class PagedKVCache:
             if not packed or t.data_ptr() % 16:
                 raise ValueError(f"{name} must be packed and 16-byte aligned"
                                  + ("" if self.rope is None else " (its token stride is free)"))
-        if out is not None and (tuple(out.shape) != tuple(q.shape) or out.dtype != torch.float32 or not out.is_contiguous()
-                                or out.get_device() != self.k_pool.get_device()):
-            raise ValueError("out must be a contiguous float32 tensor of q's shape on the cache's device")
+        if not good_out:
+            raise ValueError("out must be a contiguous, 16-byte aligned float32 tensor of q's shape on the cache's device")
         # head counts and types that the attention does not take
         LC.pkv_sparse_workspace_size(n, q.shape[1], hkv, d, 1 if max_selected is None else int(max_selected),
                                      self.block_size, self.k_pool.dtype)

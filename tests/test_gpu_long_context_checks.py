@@ -43,6 +43,7 @@ BAD = {  # a change of (q, k, v, scale, keywords), and the error
     "scale": (lambda q, k, v: (q, k, v), {"scale": math.nan}, ValueError),
     "out's shape": (lambda q, k, v: (q, k, v), {"out": (1, 8, D)}, ValueError),
     "out's type": (lambda q, k, v: (q, k, v), {"out": torch.float16}, ValueError),
+    "out misaligned": (lambda q, k, v: (q, k, v), {"out": "odd"}, ValueError),
 }
 
 
@@ -63,7 +64,8 @@ def test_a_refused_step_reserves_and_writes_nothing(what, pool, rope, bounds, ma
     free = cache.stats()
     kw = dict(kw)
     if "out" in kw:
-        kw["out"] = torch.empty(kw["out"], device="cuda") if isinstance(kw["out"], tuple) else \
+        kw["out"] = torch.empty(2 * 8 * D + 1, device="cuda")[1:].view(2, 8, D) if kw["out"] == "odd" else \
+            torch.empty(kw["out"], device="cuda") if isinstance(kw["out"], tuple) else \
             torch.empty(2, 8, D, dtype=kw["out"], device="cuda")
     args = change(*step_inputs(rows))
     if pool == torch.float32 and what == "16 heads a group":
@@ -98,6 +100,11 @@ def test_a_step_from_views_of_one_projection():
         c.refresh_bounds([0, 1])
         outs.append(c.decode_step([0, 1], *rows, 0.1, max_selected=4).clone())
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    mine = torch.empty(2, 8, D, device="cuda")
+    for c in caches:  # the same step into a tensor of the caller's, behind one of the same sizes
+        assert c.decode_step([0, 1], *parts, 0.1, max_selected=4, out=mine) is mine
+        outs.append(mine.clone())
+    assert torch.equal(outs[3], outs[4]) and torch.equal(outs[3], outs[5])
     one = caches[0].decode_step([1], x[1:, :8], x[1:, 8:10], x[1:, 10:], 0.1, max_selected=np.int64(4))
     assert one.shape == (1, 8, D)
 

@@ -85,3 +85,28 @@ def test_where_no_gradient_is_recorded(native):
     with pytest.raises(RuntimeError):  # the positions of the forward pass are gone
         y.sum().backward()
     assert np.isfinite(float(y.detach().float().sum()))
+
+
+def test_captured_forward_and_backward(native):
+    """Both passes in one graph, replayed on new contents."""
+    x, pos, inv = inputs(40, 8, 128, 128, "bf16", 2)
+    dy, _, _ = inputs(40, 8, 128, 128, "bf16", 3)
+    leaf = x.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(P.pkv_rope(leaf, pos, inv), leaf, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = P.pkv_rope(leaf, pos, inv)
+        (grad,) = torch.autograd.grad(y, leaf, dy)
+    for sign in (1, -1):
+        with torch.no_grad():
+            leaf.copy_(sign * x)
+            dy.mul_(sign)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.detach(), P.pkv_rope(sign * x, pos, inv))
+        assert torch.equal(grad, P.pkv_rope(dy, pos, inv, transpose=True))
